@@ -120,7 +120,9 @@ enum {
   IDX_E_DEVICE_CHECK = 9 /* IDX_DEBUG: a precondition in device memory failed   */
 };
 
-enum { IDX_K_FP8_E4M3 = 0, IDX_K_MXFP4 = 1 };
+/* Formats of keys and caches.  The indexer's keys are E4M3 or MXFP4; rows of values and
+ * the caches of the entry points around it also come in 16 and 32 bits. */
+enum { IDX_K_FP8_E4M3 = 0, IDX_K_MXFP4 = 1, IDX_K_BF16 = 2, IDX_K_F16 = 3, IDX_K_F32 = 4 };
 
 /* Operations for idx_workspace_size(). */
 enum {
@@ -314,6 +316,140 @@ idx_status idx_gather_rows(const idx_problem *p, const int32_t *rows, int32_t R,
  * output keeps): rows[i * n + m] = cu_q[i+1] - n + m, or -1 where request i has
  * fewer than n rows.  cu_q: device int32 [B + 1]; rows: device int32 [B * n]. */
 idx_status idx_tail_rows(const int32_t *cu_q, int32_t B, int32_t n, int32_t *rows, void *stream);
+
+/* ---- Around the indexer: rotary positions, quantised caches, attention over the selection ----
+ *
+ * A model's attention layer rotates its queries and keys, quantises the indexer's (and
+ * usually the attention's) keys as it writes them to a cache, calls the indexer, and
+ * attends to the keys the indexer selected.  The entry points below are those steps.  The
+ * conventions above hold, and these:
+ *   - Row arrays and caches have a contiguous last dimension of D; the other strides are
+ *     the caller's, in elements.  Arrays start on a 16-byte boundary, and so does every row
+ *     of values; a cache's ld is a multiple of 8 (for idx_sparse_attn, of 16 bytes).
+ *   - Slots, positions and row lists are device int32.  A slot or row outside the cache is
+ *     skipped on a write and reads as zeros; nothing outside the arrays is touched.
+ *   - A value that is not finite stays visible: a row written to E4M3, or a block of 32
+ *     written to MXFP4, that holds a NaN or an infinity reads back as NaN. */
+
+/* T x H rows of D values (IDX_K_BF16, IDX_K_F16 or IDX_K_F32), row (t, h) at
+ * data + t * ld_t + h * ld_h elements.  Input rows may share memory (stride 0). */
+typedef struct idx_rows {
+  void *data;
+  int64_t ld_t, ld_h;
+  int32_t dtype;
+  int32_t T, H, D;
+} idx_rows;
+
+/* Rotary positions of one part of the head, dims [rot0, rot0 + rot): pair i of row t is
+ * turned by the angle pos[t] * freq[i],
+ *     (a, b) -> mscale * (a cos - b sin, b cos + a sin),
+ * and turned back by it when `inverse` is set (the transpose: what a gradient, or a key
+ * that moves to another position, needs).  IDX_ROPE_HALF pairs dims rot0 + i and
+ * rot0 + rot/2 + i, IDX_ROPE_INTERLEAVED dims rot0 + 2 i and rot0 + 2 i + 1.  Angles are
+ * computed and reduced in fp64 for any int32 position; cosine and sine are rounded to fp32,
+ * their products and sum kept in fp64, and the result rounded once to fp32 and once more
+ * to the output's type. */
+enum { IDX_ROPE_HALF = 0, IDX_ROPE_INTERLEAVED = 1 };
+typedef struct idx_rotary {
+  const double *freq;   /* [rot / 2] radians a position (idx_rope_freqs)        */
+  const int32_t *pos;   /* [T] position of each row, any sign                   */
+  int32_t rot, rot0;    /* multiples of 8, 8 <= rot, rot0 + rot <= D            */
+  int32_t layout;       /* IDX_ROPE_HALF or IDX_ROPE_INTERLEAVED                */
+  int32_t inverse;
+  double mscale;        /* gain on the rotated values (1.0 if unused)           */
+} idx_rotary;
+
+/* Pair frequencies, written to host memory (freq: [rot / 2]): freq[i] = base^(-2 i / rot), and for
+ * a context of `original` positions stretched by `factor`:
+ *   IDX_ROPE_LINEAR  freq[i] / factor;
+ *   IDX_ROPE_BASE    base * factor^(rot / (rot - 2)) in place of base;
+ *   IDX_ROPE_PARTS   freq[i] (1 - r) + freq[i] / factor * r, r rising from 0 at the pair that makes
+ *                    beta_fast turns over `original` positions to 1 at the one that makes beta_slow
+ *                    (pair numbers rounded outwards); *mscale = 0.1 ln(factor) + 1.
+ * *mscale (nullable) is 1 for the others.  factor, original and the betas are read only where used.
+ * Host only; touches no device. */
+enum { IDX_ROPE_PLAIN = 0, IDX_ROPE_LINEAR = 1, IDX_ROPE_BASE = 2, IDX_ROPE_PARTS = 3 };
+idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double factor, double original,
+                          double beta_fast, double beta_slow, double *freq, double *mscale);
+
+/* Rows of x rotated into out (same sizes and type).  out may be x itself, with the same
+ * strides; otherwise the two share no byte.  D a multiple of 8, at most 512. */
+idx_status idx_rope(const idx_rows *x, const idx_rotary *r, const idx_rows *out, void *stream);
+
+/* A cache of `rows` slots with H rows of D values each; slot s, head h at s * ld + h * D elements.
+ *   IDX_K_FP8_E4M3  one byte a value; scale: float, (s, h) at s * ld_scale + h; value = code * scale
+ *   IDX_K_MXFP4     two values a byte, the even one in the low nibble; scale: uint8 E8M0, one per 32
+ *                   values, block b of (s, h) at s * ld_scale + h * D / 32 + b (D a multiple of 32)
+ *   IDX_K_BF16, IDX_K_F16, IDX_K_F32  the values; no scale
+ * With H = 1 and D = 128 the first two are idx_problem's k and k_scale, and an E4M3 cache of T
+ * slots with H = 32 or 64 is its q and q_scale (ld = H * D, ld_scale = H or H * D / 32). */
+typedef struct idx_cache {
+  void *data;
+  void *scale;
+  int64_t rows;
+  int64_t ld, ld_scale;
+  int32_t fmt;
+  int32_t H, D;
+} idx_cache;
+
+/* One array of rows on its way into a cache: row (t, h) of x, rotated if `rotary` is not NULL, is
+ * quantised and stored to slot slot[t] (t itself where slot is NULL).  E4M3: amax the row's largest
+ * magnitude, scale = amax / 448 and code = x * (448 / amax) in fp32, rounded to nearest even (a row
+ * with amax < 2^-100: zeros, scale 1).  MXFP4: exponent floor(log2 amax) - 2 of each 32 values,
+ * codes rounded to nearest even and saturating at 6 (a block with amax < 2^-100: zeros, E8M0 code
+ * 0).  The other formats round to nearest even. */
+typedef struct idx_write {
+  idx_rows x;
+  const idx_rotary *rotary; /* nullable; read during the call only */
+  const int32_t *slot;      /* nullable: [T]                       */
+  idx_cache to;
+} idx_write;
+
+/* Up to IDX_MAX_WRITES of them in one launch (a serving step's indexer query and key, attention key
+ * and value).  The slots of one cache named in a call are distinct (IDX_DEBUG checks each array's):
+ * a slot named twice holds bytes of either row.  The caches share no byte with the inputs. */
+#define IDX_MAX_WRITES 8
+idx_status idx_cache_write(const idx_write *w, int32_t n, void *stream);
+
+/* Rows of a cache as values: out row (t, h) = slot rows[t], head h (t itself where rows is NULL), the
+ * product code * scale in fp32 rounded to out's type; zeros where rows[t] is outside the cache. */
+idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_rows *out, void *stream);
+
+/* Attention of each query row over its selected keys:
+ *     out[t, h, :] = sum_i p_i v[row_i, h / G, :],  p = softmax_i(scale * <q[t, h, :], k[row_i, h / G, :]>),
+ * G = Hq / H query heads to a cache head (consecutive ones), i over the entries of the row's list that
+ * count.  lse (nullable): [T, Hq] fp32, ln of the sum of the exponentials, -inf for a row in which
+ * nothing counts; its out is zeros.
+ *   pool = 1: sel[t * ld_sel + i], i < n_sel, are keys (out_idx of the indexer), and count if
+ *     0 <= id < L and, with windows, ks[t] <= id < ke[t].
+ *   pool > 1 (a power of two up to 64): they are blocks (out_blocks of idx_block_candidates, pool 8);
+ *     block b >= 0 stands for the keys ks[t] + pool b ... + pool - 1 below ke[t] (and below L).
+ * A key's cache row is the key itself, or slot_of_key[key] where that table (int32 [L]) is given; a
+ * row outside the caches does not count.  Every entry is a term of its own: an id listed twice counts
+ * twice.  Rows that do not count are not read, so what they hold reaches no output.  The order of
+ * entries has no influence beyond the rounding of sums; results are bitwise repeatable.
+ * q and out share type and sizes, IDX_K_BF16 or IDX_K_F16; the caches are of that type or E4M3, both
+ * alike; D = 64 or 128.  Products run on the matrix cores with fp32 accumulation, E4M3 codes
+ * converted exactly; weights are rounded to 16 bits before the second product (2^-9 relative in
+ * bf16, 2^-12 in fp16: bf16 wherever v is E4M3), sums and maxima are fp32.
+ * ws: idx_sparse_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap
+ * in time need one each. */
+typedef struct idx_attn {
+  idx_rows q;
+  idx_rows out;
+  idx_cache k, v;
+  const int32_t *sel;
+  int64_t ld_sel;
+  int32_t n_sel;
+  int32_t pool;
+  const int32_t *ks, *ke;       /* [T]; both NULL (pool = 1 only) or both given */
+  const int32_t *slot_of_key;   /* nullable                                     */
+  int32_t L;                    /* keys; at most k.rows without a table          */
+  float scale;
+  float *lse;                   /* nullable                                     */
+} idx_attn;
+idx_status idx_sparse_attn_workspace(const idx_attn *a, size_t *bytes);
+idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *stream);
 
 /* Launch timing, for benchmarks and profilers (P3: the chunk-budget and CPU-gap
  * commits attribute the indexer's time to its kernels).  idx_launch_timing(1) clears

@@ -7,7 +7,9 @@ none) and the current HIP stream.  There is no fallback: if libidx.so is
 missing or fails to load, every call raises.
 
 Function names match the C entry points.  Tensors must be on the GPU and
-contiguous; key indices in outputs are absolute rows of k.
+contiguous; key indices in outputs are absolute rows of k.  The operators around
+the indexer (idx_rope, idx_cache_write, idx_cache_read, idx_sparse_attn) check
+types, shapes and devices here, and take any strides the C entry points take.
 """
 from __future__ import annotations
 
@@ -23,6 +25,16 @@ LIB_PATH = os.path.join(_HERE, "libidx.so")
 
 IDX_K_FP8_E4M3 = 0
 IDX_K_MXFP4 = 1
+IDX_K_BF16 = 2
+IDX_K_F16 = 3
+IDX_K_F32 = 4
+IDX_ROPE_HALF = 0
+IDX_ROPE_INTERLEAVED = 1
+IDX_ROPE_PLAIN = 0
+IDX_ROPE_LINEAR = 1
+IDX_ROPE_BASE = 2
+IDX_ROPE_PARTS = 3
+IDX_MAX_WRITES = 8
 IDX_OP_MQA_LOGITS = 0
 IDX_OP_TOPK = 1
 IDX_OP_LOGITS_TOPK_FUSED = 2
@@ -37,7 +49,9 @@ EXPORTS = ("idx_mqa_logits", "idx_mqa_logits_block", "idx_topk", "idx_logits_top
            "idx_logits_topk_fused_paged", "idx_logits_topk_fused_blocks", "idx_logits_topk_fused_static",
            "idx_refine_topk",
            "idx_block_candidates", "idx_workspace_size", "idx_ragged_windows", "idx_ragged_windows_ratio",
-           "idx_gather_rows", "idx_tail_rows", "idx_launch_timing", "idx_launch_timing_read", "idx_status_str")
+           "idx_gather_rows", "idx_tail_rows", "idx_rope_freqs", "idx_rope", "idx_cache_write", "idx_cache_read",
+           "idx_sparse_attn_workspace", "idx_sparse_attn", "idx_launch_timing", "idx_launch_timing_read",
+           "idx_status_str")
 
 IDX_TIMING_MAX = 1024
 LAUNCH_MODES = {0: "dense", 1: "block", 2: "pool8", 4: "slab"}
@@ -60,6 +74,35 @@ class idx_problem(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("k_fmt", ctypes.c_int32), ("w", ctypes.c_void_p),
                 ("ks", ctypes.c_void_p), ("ke", ctypes.c_void_p), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("L", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class idx_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld_t", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class idx_rotary(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("rot", ctypes.c_int32),
+                ("rot0", ctypes.c_int32), ("layout", ctypes.c_int32), ("inverse", ctypes.c_int32),
+                ("mscale", ctypes.c_double)]
+
+
+class idx_cache(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("ld_scale", ctypes.c_int64), ("fmt", ctypes.c_int32),
+                ("H", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
+class idx_write(ctypes.Structure):
+    _fields_ = [("x", idx_rows), ("rotary", ctypes.POINTER(idx_rotary)), ("slot", ctypes.c_void_p),
+                ("to", idx_cache)]
+
+
+class idx_attn(ctypes.Structure):
+    _fields_ = [("q", idx_rows), ("out", idx_rows), ("k", idx_cache), ("v", idx_cache), ("sel", ctypes.c_void_p),
+                ("ld_sel", ctypes.c_int64), ("n_sel", ctypes.c_int32), ("pool", ctypes.c_int32),
+                ("ks", ctypes.c_void_p), ("ke", ctypes.c_void_p), ("slot_of_key", ctypes.c_void_p),
+                ("L", ctypes.c_int32), ("scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
 
 
 _lib = None
@@ -89,6 +132,14 @@ def load_library():
     lib.idx_ragged_windows_ratio.argtypes = [VP, VP, VP, i32, i32, i32, VP, VP, VP]
     lib.idx_gather_rows.argtypes = [P, VP, i32, P, VP, sz, VP]
     lib.idx_tail_rows.argtypes = [VP, i32, i32, VP, VP]
+    f64, pf64 = ctypes.c_double, ctypes.POINTER(ctypes.c_double)
+    R, C = ctypes.POINTER(idx_rows), ctypes.POINTER(idx_cache)
+    lib.idx_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, pf64, pf64]
+    lib.idx_rope.argtypes = [R, ctypes.POINTER(idx_rotary), R, VP]
+    lib.idx_cache_write.argtypes = [ctypes.POINTER(idx_write), i32, VP]
+    lib.idx_cache_read.argtypes = [C, VP, R, VP]
+    lib.idx_sparse_attn_workspace.argtypes = [ctypes.POINTER(idx_attn), ctypes.POINTER(sz)]
+    lib.idx_sparse_attn.argtypes = [ctypes.POINTER(idx_attn), VP, sz, VP]
     lib.idx_launch_timing.argtypes = [i32]
     lib.idx_launch_timing_read.argtypes = [ctypes.POINTER(idx_launch_time), i32, ctypes.POINTER(i32)]
     lib.idx_status_str.argtypes = [i32]
@@ -435,3 +486,255 @@ def idx_launch_timing_read() -> list:
 
 def idx_status_str(status: int) -> str:
     return status_str(status)
+
+
+# ---- around the indexer: rotary positions, quantised caches, attention over the selection ----
+
+_VALUE = {torch.bfloat16: IDX_K_BF16, torch.float16: IDX_K_F16, torch.float32: IDX_K_F32}
+_STORED = {IDX_K_FP8_E4M3: torch.uint8, IDX_K_MXFP4: torch.uint8, IDX_K_BF16: torch.bfloat16,
+           IDX_K_F16: torch.float16, IDX_K_F32: torch.float32}
+
+
+def _want(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _on(t: torch.Tensor, device, dtype, what: str) -> int:
+    """The tensor's address, if it is one the kernels can read as it stands."""
+    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _rows(x: torch.Tensor, what: str) -> idx_rows:
+    if not x.is_cuda or x.dim() != 3 or x.dtype not in _VALUE or (x.shape[2] > 1 and x.stride(2) != 1):
+        raise ValueError(f"{what}: [T, H, D] bfloat16, float16 or float32 on the GPU with a contiguous last "
+                         f"dimension, got {list(x.shape)} {x.dtype} on {x.device}, strides {x.stride()}")
+    T, H, D = x.shape
+    return idx_rows(x.data_ptr(), x.stride(0), x.stride(1), _VALUE[x.dtype], T, H, D)
+
+
+class _Stream:
+    """The call's stream: the one given, or the current one of the tensors' device.  Outputs and
+    workspaces allocated inside belong to it."""
+
+    def __init__(self, device: torch.device, stream):
+        self.guard = None
+        if stream is not None:
+            _want(stream.device == device, f"a stream of {stream.device} for tensors on {device}")
+            self.guard = torch.cuda.stream(stream)
+        elif device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.device, self.stream = device, stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
+        return ctypes.c_void_p(stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def idx_rope_freqs(rot: int, base: float = 10000.0, scaling: int = IDX_ROPE_PLAIN, factor: float = 1.0,
+                   original: float = 1.0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Pair frequencies (a CPU float64 tensor [rot / 2]) and the gain that goes with them."""
+    out, gain = (ctypes.c_double * max(rot // 2, 1))(), ctypes.c_double()
+    _check("idx_rope_freqs", load_library().idx_rope_freqs(rot, base, scaling, factor, original, beta_fast, beta_slow,
+                                                           out, ctypes.byref(gain)))
+    return torch.tensor(list(out), dtype=torch.float64), gain.value
+
+
+class Rotary:
+    """Rotary positions of dims [rot0, rot0 + 2 len(freq)) of a head; keep one and pass it to every call."""
+
+    def __init__(self, freq: torch.Tensor, rot0: int = 0, layout: int = IDX_ROPE_HALF, mscale: float = 1.0):
+        _want(freq.is_cuda and freq.dim() == 1, f"freq: one dimension, on the GPU, got {list(freq.shape)} on "
+              f"{freq.device}")
+        self.freq, self.rot0, self.layout, self.mscale = freq, rot0, layout, mscale
+        self._args = (_on(freq, freq.device, torch.float64, "freq"), 2 * int(freq.numel()), rot0, layout, mscale)
+
+    @staticmethod
+    def make(rot: int, device="cuda", rot0: int = 0, layout: int = IDX_ROPE_HALF, **scaling) -> "Rotary":
+        """From idx_rope_freqs's arguments."""
+        freq, mscale = idx_rope_freqs(rot, **scaling)
+        return Rotary(freq.to(device), rot0=rot0, layout=layout, mscale=mscale)
+
+    def struct(self, pos: torch.Tensor, x: torch.Tensor, inverse: bool = False) -> idx_rotary:
+        freq, rot, rot0, layout, mscale = self._args
+        _want(pos is not None and pos.shape == x.shape[:1], "pos: [T], one position a row")
+        _want(self.freq.device == x.device, f"a Rotary on {self.freq.device} for rows on {x.device}")
+        return idx_rotary(freq, _on(pos, x.device, torch.int32, "pos"), rot, rot0, layout, int(inverse), mscale)
+
+
+class Cache:
+    """A cache of slots of H heads of D values (include/idx.h, idx_cache); keep one and pass it to
+    every call.  data: [slots, H, D] of the format's type, MXFP4 uint8 [slots, H, D / 2]; scale:
+    float32 [slots, H] for E4M3, uint8 [slots, H, D / 32] for MXFP4, else None.  A head's values
+    follow each other, and so do a slot's heads; slots may be further apart."""
+
+    def __init__(self, data: torch.Tensor, scale: Optional[torch.Tensor] = None, D: Optional[int] = None,
+                 fmt: int = IDX_K_FP8_E4M3):
+        _want(fmt in _STORED, f"unknown cache format {fmt}")
+        _want(data.is_cuda and data.dim() == 3 and data.dtype == _STORED[fmt],
+              f"cache data: [slots, H, D] {_STORED[fmt]} on the GPU, got {list(data.shape)} {data.dtype} on "
+              f"{data.device}")
+        rows, H, width = data.shape
+        D = width * (2 if fmt == IDX_K_MXFP4 else 1) if D is None else D
+        _want(width == (D // 2 if fmt == IDX_K_MXFP4 else D), f"cache data: {width} wide for D = {D}")
+        _want(width <= 1 or data.stride(2) == 1, "cache data: a contiguous last dimension")
+        _want(H <= 1 or data.stride(1) == width, "cache data: a slot's heads follow each other")
+        ld_scale, shape = 0, {IDX_K_FP8_E4M3: (rows, H), IDX_K_MXFP4: (rows, H, D // 32)}.get(fmt)
+        if shape is not None:
+            want = torch.float32 if fmt == IDX_K_FP8_E4M3 else torch.uint8
+            _want(scale is not None and scale.device == data.device and scale.dtype == want
+                  and tuple(scale.shape) == shape, f"cache scale: {list(shape)} {want} on {data.device}")
+            inner = scale[:1]
+            _want(rows == 0 or inner.is_contiguous(), "cache scale: a slot's scales follow each other")
+            ld_scale = scale.stride(0)
+        else:
+            _want(scale is None, "a 16- or 32-bit cache has no scale")
+        self.data, self.scale, self.fmt, self.D = data, scale, fmt, D
+        self.device = data.device
+        ld = data.stride(0) * (2 if fmt == IDX_K_MXFP4 else 1)
+        self._args = (data.data_ptr(), None if scale is None else scale.data_ptr(), rows, ld, ld_scale, fmt, H, D)
+
+    @staticmethod
+    def empty(rows: int, H: int, D: int, fmt: int = IDX_K_FP8_E4M3, device="cuda") -> "Cache":
+        """A cache of zeros."""
+        _want(fmt in _STORED, f"unknown cache format {fmt}")
+        data = torch.zeros((rows, H, D // 2 if fmt == IDX_K_MXFP4 else D), dtype=_STORED[fmt], device=device)
+        scale = None
+        if fmt == IDX_K_FP8_E4M3:
+            scale = torch.ones((rows, H), dtype=torch.float32, device=device)
+        elif fmt == IDX_K_MXFP4:
+            scale = torch.zeros((rows, H, D // 32), dtype=torch.uint8, device=device)
+        return Cache(data, scale, D=D, fmt=fmt)
+
+    @property
+    def rows(self) -> int:
+        return int(self.data.shape[0])
+
+    @property
+    def H(self) -> int:
+        return int(self.data.shape[1])
+
+    def struct(self) -> idx_cache:
+        return idx_cache(*self._args)
+
+
+@dataclass
+class Write:
+    """One array of rows [T, H, D] on its way into a cache (include/idx.h, idx_write)."""
+    x: torch.Tensor
+    cache: Cache
+    slot: Optional[torch.Tensor] = None     # int32 [T]; None: row t to slot t
+    rotary: Optional[Rotary] = None
+    pos: Optional[torch.Tensor] = None      # int32 [T], with a rotary
+    inverse: bool = False
+
+
+def idx_rope(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, out: Optional[torch.Tensor] = None,
+             inverse: bool = False, stream=None) -> torch.Tensor:
+    """x [T, H, D] rotated to positions pos [T]; out may be x."""
+    rows, r = _rows(x, "x"), rotary.struct(pos, x, inverse)
+    with _Stream(x.device, stream) as st:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _want(out.device == x.device, f"out on {out.device} for x on {x.device}")
+        to = _rows(out, "out")
+        _check("idx_rope", load_library().idx_rope(rows, r, to, st))
+    return out
+
+
+def idx_cache_write(writes, stream=None) -> None:
+    """Rotate (where asked), quantise and store every Write's rows, in one launch."""
+    n = len(writes)
+    _want(n <= IDX_MAX_WRITES, f"{n} writes in a call, at most {IDX_MAX_WRITES}")
+    if n == 0:
+        return
+    device = writes[0].x.device
+    args, keep = (idx_write * n)(), []
+    for a, w in zip(args, writes):
+        a.x = _rows(w.x, "x")
+        _want(w.x.device == device and w.cache.device == device, "every row array and cache of a call on one device")
+        if w.rotary is not None:
+            keep.append(w.rotary.struct(w.pos, w.x, w.inverse))
+            a.rotary = ctypes.pointer(keep[-1])
+        if w.slot is not None:
+            _want(w.slot.shape == w.x.shape[:1], "slot: [T], one slot a row")
+            a.slot = _on(w.slot, device, torch.int32, "slot")
+        a.to = w.cache.struct()
+    with _Stream(device, stream) as st:
+        _check("idx_cache_write", load_library().idx_cache_write(args, n, st))
+
+
+def idx_cache_read(cache: Cache, rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """Values [N, H, D] of the slots rows [N] (None: every slot in order); zeros for a slot outside the cache."""
+    device = cache.device
+    at = None
+    if rows is not None:
+        _want(rows.dim() == 1, "rows: one dimension")
+        at = _on(rows, device, torch.int32, "rows")
+    n = cache.rows if rows is None else int(rows.shape[0])
+    with _Stream(device, stream) as st:
+        if out is None:
+            out = torch.empty((n, cache.H, cache.D), dtype=dtype, device=device)
+        else:
+            _want(out.device == device and out.shape[0] == n, f"out: {n} rows on {device}")
+        to = _rows(out, "out")
+        _check("idx_cache_read", load_library().idx_cache_read(cache.struct(), at, to, st))
+    return out
+
+
+def idx_sparse_attn(q: torch.Tensor, k: Cache, v: Cache, sel: torch.Tensor, scale: float, pool: int = 1,
+                    ks: Optional[torch.Tensor] = None, ke: Optional[torch.Tensor] = None,
+                    slot_of_key: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, with_lse: bool = True,
+                    stream=None):
+    """Attention of q [T, Hq, D] over the keys (pool 1) or blocks of keys that sel [T, n] lists; (out, lse)."""
+    device = q.device
+    T, Hq, _ = q.shape if q.dim() == 3 else (0, 0, 0)
+    a = idx_attn(q=_rows(q, "q"), k=k.struct(), v=v.struct(), pool=pool, scale=scale)
+    _want(k.device == device and v.device == device, f"caches on {k.device} and {v.device} for q on {device}")
+    if (sel.device != device or sel.dtype != torch.int32 or sel.dim() != 2 or sel.shape[0] != T
+            or (sel.shape[1] > 1 and sel.stride(1) != 1)):
+        raise ValueError(f"sel: [T, n] int32 on {device} with a contiguous last dimension, got {list(sel.shape)} "
+                         f"{sel.dtype} on {sel.device}")
+    a.sel, a.ld_sel, a.n_sel = sel.data_ptr(), sel.stride(0), sel.shape[1]
+    if ks is not None or ke is not None:
+        _want(ks is not None and ke is not None and ks.shape == (T,) and ke.shape == (T,), "ks and ke: [T] both")
+        a.ks, a.ke = _on(ks, device, torch.int32, "ks"), _on(ke, device, torch.int32, "ke")
+    if slot_of_key is None:
+        a.L = k.rows
+    else:
+        _want(slot_of_key.dim() == 1, "slot_of_key: one dimension")
+        a.L, a.slot_of_key = slot_of_key.shape[0], _on(slot_of_key, device, torch.int32, "slot_of_key")
+    lib = load_library()
+    with _Stream(device, stream) as st:
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        else:
+            _want(out.device == device, f"out on {out.device} for q on {device}")
+        if lse is None:
+            if with_lse:
+                lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
+        else:
+            _want(lse.shape == (T, Hq), f"lse: {[T, Hq]}")
+        a.out = _rows(out, "out")
+        if lse is not None:
+            a.lse = _on(lse, device, torch.float32, "lse")
+        need = ctypes.c_size_t()
+        _check("idx_sparse_attn_workspace", lib.idx_sparse_attn_workspace(a, need))
+        if ws is None:
+            ws = _workspace(need.value, device)
+        else:
+            _on(ws, device, torch.uint8, "ws")
+        _check("idx_sparse_attn", lib.idx_sparse_attn(a, _ptr(ws), 0 if ws is None else ws.numel(), st))
+    return out, lse

@@ -31,6 +31,10 @@ bool exact_enabled();
 idx_status debug_check(const int32_t *ks, const int32_t *ke, int32_t T, int32_t L, int64_t W, const idx_problem *p,
                        void *stream);
 
+// In debug mode: check on the device that no slot of slot[0, T) inside [0, rows) is named twice; as debug_check
+// otherwise (slot nullable: nothing to check).
+idx_status debug_check_slots(const int32_t *slot, int32_t T, int64_t rows, void *stream);
+
 // Launch timing (idx_launch_timing): timing_begin records a launch's first event on s when a
 // record is on, and returns a token for its slot (-1: not recorded); timing_end records the
 // second event (ok: the launch was enqueued) and the launch's description.

@@ -17,6 +17,7 @@
 
 #include "../../include/idx.h"
 #include "api_internal.h"
+#include "rows.h"
 
 static __device__ uint32_t debug_word[1];
 
@@ -84,6 +85,15 @@ __global__ void check_keys_kernel(const uint8_t *k_scale, int32_t k_fmt, int32_t
   if (bad) atomicOr(word, bad);
 }
 
+// Waits for the checks enqueued on s and reads their result.
+idx_status verdict(const uint32_t *word, hipStream_t s) {
+  if (hipGetLastError() != hipSuccess) return IDX_E_LAUNCH;
+  uint32_t host = 0;
+  if (hipMemcpyAsync(&host, word, sizeof(host), hipMemcpyDeviceToHost, s) != hipSuccess) return IDX_E_LAUNCH;
+  if (hipStreamSynchronize(s) != hipSuccess) return IDX_E_LAUNCH;
+  return host ? IDX_E_DEVICE_CHECK : IDX_OK;
+}
+
 }  // namespace
 
 namespace idx {
@@ -118,11 +128,17 @@ idx_status debug_check(const int32_t *ks, const int32_t *ke, int32_t T, int32_t 
     hipLaunchKernelGGL(check_keys_kernel, dim3(blocks), dim3(256), 0, s, (const uint8_t *)p->k_scale, p->k_fmt,
                        p->L, word);
   }
-  if (hipGetLastError() != hipSuccess) return IDX_E_LAUNCH;
-  uint32_t host = 0;
-  if (hipMemcpyAsync(&host, word, sizeof(host), hipMemcpyDeviceToHost, s) != hipSuccess) return IDX_E_LAUNCH;
-  if (hipStreamSynchronize(s) != hipSuccess) return IDX_E_LAUNCH;
-  return host ? IDX_E_DEVICE_CHECK : IDX_OK;
+  return verdict(word, s);
+}
+
+idx_status debug_check_slots(const int32_t *slot, int32_t T, int64_t rows, void *stream) {
+  if (!debug_enabled() || !slot || T <= 0) return IDX_OK;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t *word = nullptr;
+  if (word_address(&word) != hipSuccess) return IDX_E_LAUNCH;
+  hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, s, word);
+  if (launch_slot_check(slot, T, rows, word, s) != hipSuccess) return IDX_E_LAUNCH;
+  return verdict(word, s);
 }
 
 }  // namespace idx

@@ -1,0 +1,373 @@
+// Rows on their way into and out of caches.
+//  - write: rotary positions, then E4M3 / MXFP4 / 16- or 32-bit storage at a slot.  idx_rope is
+//    this kernel with a 16- or 32-bit output and no slots.
+//  - read: cache rows as values, by slot.
+// Both move each byte once and are bound by memory (or, for a few rows, by the launch).
+#include "common.h"
+#include "rows.h"
+
+namespace idx {
+namespace {
+
+constexpr int HEADS = 4;       // heads a lane takes of one token: they share the sines and cosines
+constexpr int THREADS = 256;
+
+struct Raw {
+  uint4 a, b;   // 8 elements: 16 bytes in a, or 32 bytes in a and b (fp32)
+};
+
+__device__ __forceinline__ float bf16_val(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float f16_val(uint32_t u) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)u);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+  const v2 p = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, p);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+  const v2 p = {(_Float16)lo, (_Float16)hi};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+// Four 16-bit or fp32 values of a word group.
+__device__ __forceinline__ void unpack4(uint32_t w0, uint32_t w1, int dtype, float *v) {
+  if (dtype == IDX_K_BF16) {
+    v[0] = bf16_val(w0 & 0xFFFFu);
+    v[1] = __uint_as_float(w0 & 0xFFFF0000u);
+    v[2] = bf16_val(w1 & 0xFFFFu);
+    v[3] = __uint_as_float(w1 & 0xFFFF0000u);
+  } else {
+    v[0] = f16_val(w0 & 0xFFFFu);
+    v[1] = f16_val(w0 >> 16);
+    v[2] = f16_val(w1 & 0xFFFFu);
+    v[3] = f16_val(w1 >> 16);
+  }
+}
+
+// The lane's 8 elements: two groups of four at element offsets e0 and e1 (e1 = e0 + 4 unless the
+// lane holds both halves of four rotated pairs).
+__device__ __forceinline__ Raw load8(const uint8_t *p, int dtype, int e0, int e1, bool split) {
+  Raw r;
+  if (dtype == IDX_K_F32) {
+    r.a = *(const uint4 *)(p + 4 * e0);
+    r.b = *(const uint4 *)(p + 4 * e1);
+  } else if (split) {
+    const uint2 lo = *(const uint2 *)(p + 2 * e0), hi = *(const uint2 *)(p + 2 * e1);
+    r.a = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+  } else {
+    r.a = *(const uint4 *)(p + 2 * e0);
+    r.b = make_uint4(0u, 0u, 0u, 0u);
+  }
+  return r;
+}
+__device__ __forceinline__ void values8(const Raw &r, int dtype, float *v) {
+  if (dtype == IDX_K_F32) {
+    v[0] = __uint_as_float(r.a.x);
+    v[1] = __uint_as_float(r.a.y);
+    v[2] = __uint_as_float(r.a.z);
+    v[3] = __uint_as_float(r.a.w);
+    v[4] = __uint_as_float(r.b.x);
+    v[5] = __uint_as_float(r.b.y);
+    v[6] = __uint_as_float(r.b.z);
+    v[7] = __uint_as_float(r.b.w);
+  } else {
+    unpack4(r.a.x, r.a.y, dtype, v);
+    unpack4(r.a.z, r.a.w, dtype, v + 4);
+  }
+}
+
+// Largest of x over aligned groups of 2^sh lanes.
+__device__ __forceinline__ uint32_t group_max(uint32_t x, int sh) {
+  if (sh > 0) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, false));
+  if (sh > 1) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, false));
+  if (sh > 2) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x141, 0xF, 0xF, false));
+  if (sh > 3) x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x140, 0xF, 0xF, false));
+  if (sh > 4) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(r[0], r[1]);
+  }
+  if (sh > 5) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(r[0], r[1]);
+  }
+  return x;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(const float *v) {
+  int w = 0;
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], w, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+  return (uint32_t)w;
+}
+
+// E2M1 code of |a| (ties to the even code), sign from x.
+__device__ __forceinline__ uint32_t e2m1(float x) {
+  const float a = __builtin_fabsf(x);
+  const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
+  return c | (x < 0.f ? 8u : 0u);
+}
+
+constexpr uint32_t TINY = 0x0D800000u;   // bits of 2^-100
+constexpr uint32_t INF = 0x7F800000u;
+
+__global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
+  int ji = 0;
+  while (ji + 1 < jobs.n && (int)blockIdx.x >= jobs.first[ji + 1]) ++ji;
+  const RowJob &j = jobs.job[ji];
+  const int sh = j.lanes_sh;
+  const int64_t unit = ((int64_t)((int)blockIdx.x - jobs.first[ji]) * THREADS + threadIdx.x) >> sh;
+  const int c = threadIdx.x & ((1 << sh) - 1);
+  const int64_t t64 = unit / j.groups;
+  const int hs = (int)(unit - t64 * j.groups);
+  if (t64 >= j.T) return;        // whole lane groups leave together
+  const int t = (int)t64;
+  const bool live = c * 8 < j.D;
+  const int64_t slot = j.slot ? (int64_t)j.slot[t] : (int64_t)t;
+  if (slot < 0 || slot >= j.rows) return;
+
+  // this lane's elements, and its pairs
+  int e0 = c * 8, e1 = e0 + 4;
+  const int part = e0 - j.rot0;
+  const bool turned = j.freq && part >= 0 && part < j.rot && live;
+  const bool split = turned && j.half;
+  if (split) {
+    e0 = j.rot0 + part / 2;
+    e1 = e0 + j.rot / 2;
+  }
+  Raw raw[HEADS];
+  const uint8_t *xt = j.x + (int64_t)t * j.x_t;
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int h = hs + i * j.groups;
+    if (live && h < j.H) raw[i] = load8(xt + (int64_t)h * j.x_h, j.dtype, e0, e1, split);
+  }
+  float cs[4], sn[4];
+  if (turned) {
+    const double p = (double)j.pos[t];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      double s, k;
+      sincos(p * j.freq[part / 2 + i], &s, &k);
+      cs[i] = (float)(k * j.mscale);
+      sn[i] = (float)(s * j.mscale);
+      if (j.inverse) sn[i] = -sn[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int h = hs + i * j.groups;
+    if (h >= j.H) break;         // the same for the whole lane group
+    float v[8];
+    if (live) {
+      values8(raw[i], j.dtype, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        // fp64: the fp32 products are exact there, so the result is rounded once
+        const int ia = split ? e : 2 * e, ib = split ? 4 + e : 2 * e + 1;
+        const double a = v[ia], b = v[ib], ck = cs[e], sk = sn[e];
+        v[ia] = (float)(a * ck - b * sk);
+        v[ib] = (float)(b * ck + a * sk);
+      }
+    }
+    uint8_t *o = j.out + slot * j.out_t + (int64_t)h * j.out_h;
+    if (j.fmt == IDX_K_FP8_E4M3) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      m = group_max(m, sh);
+      const float amax = __uint_as_float(m);
+      const bool some = m >= TINY;
+      const float inv = some ? 448.0f / amax : 0.f;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = v[e] * inv;
+      if (live) {
+        const uint32_t w0 = e4m3x4(y), w1 = e4m3x4(y + 4);
+        if (split) {
+          *(uint32_t *)(o + e0) = w0;
+          *(uint32_t *)(o + e1) = w1;
+        } else {
+          *(uint2 *)(o + e0) = make_uint2(w0, w1);
+        }
+        // a NaN or an infinity in the row makes the scale NaN, and with it the whole row
+        if (c == 0)
+          *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
+              m >= INF ? __uint_as_float(0x7FC00000u) : some ? amax / 448.0f : 1.0f;
+      }
+    } else if (j.fmt == IDX_K_MXFP4) {
+      // The lane's two groups of four lie in blocks of 32 of their own when it holds the halves of
+      // pairs: bring the values back into order, lane c holding elements 8c .. 8c + 7.
+      if (j.freq && j.half) {
+        const int lo = (j.rot0 >> 3), n = j.rot >> 3;        // rotated lanes [lo, lo + n)
+        const int base = (threadIdx.x & 63) - c;
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int q = 2 * (c - lo) + (e >> 2);             // group of four inside the part
+          const bool in = c >= lo && c < lo + n;
+          const int src = in ? lo + (q < n ? q : q - n) : c;
+          const float va = __shfl(v[e & 3], base + src), vb = __shfl(v[4 + (e & 3)], base + src);
+          w[e] = in ? (q < n ? va : vb) : v[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = w[e];
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      m = group_max(m, 2);       // 4 lanes hold a block of 32
+      const int ex = (int)(m >> 23) - 127 - 2;
+      const int e8 = m >= TINY ? min(max(ex + 127, 0), 254) : 0;
+      const float inv = m >= TINY ? __uint_as_float((uint32_t)(254 - e8) << 23) : 0.f;
+      if (live) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w |= e2m1(v[e] * inv) << (4 * e);
+        *(uint32_t *)(o + c * 4) = w;
+        if ((c & 3) == 0)
+          j.scale[slot * j.scale_t + (int64_t)h * j.scale_h + (c >> 2)] = m >= INF ? 0xFFu : (uint8_t)e8;
+      }
+    } else if (live) {
+      if (j.fmt == IDX_K_F32) {
+        *(float4 *)(o + 4 * e0) = make_float4(v[0], v[1], v[2], v[3]);
+        *(float4 *)(o + 4 * e1) = make_float4(v[4], v[5], v[6], v[7]);
+      } else {
+        uint4 w;
+        if (j.fmt == IDX_K_BF16)
+          w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+        else
+          w = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+        if (split) {
+          *(uint2 *)(o + 2 * e0) = make_uint2(w.x, w.y);
+          *(uint2 *)(o + 2 * e1) = make_uint2(w.z, w.w);
+        } else {
+          *(uint4 *)(o + 2 * e0) = w;
+        }
+      }
+    }
+  }
+}
+
+__device__ __constant__ const float E2M1_VALUE[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
+
+// One lane to 8 elements of a row.
+__global__ __launch_bounds__(THREADS) void read_kernel(ReadJob j) {
+  const int n = j.D / 8;
+  const int64_t per = (int64_t)j.H * n;
+  const int64_t x = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+  if (x >= (int64_t)j.T * per) return;
+  const int t = (int)(x / per);
+  const int r = (int)(x - t * per);
+  const int h = r / n, c = r - h * n;
+  const int64_t row = j.list ? (int64_t)j.list[t] : (int64_t)t;
+  float v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  if (row >= 0 && row < j.rows) {
+    const uint8_t *p = j.data + row * j.data_t + (int64_t)h * j.data_h;
+    const uint8_t *s = j.scale + row * j.scale_t + (int64_t)h * j.scale_h;
+    if (j.fmt == IDX_K_FP8_E4M3) {
+      const uint2 w = *(const uint2 *)(p + 8 * c);
+      const float sc = *(const float *)s;
+      const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
+      const auto d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false), f = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+      v[0] = a[0] * sc;
+      v[1] = a[1] * sc;
+      v[2] = b[0] * sc;
+      v[3] = b[1] * sc;
+      v[4] = d[0] * sc;
+      v[5] = d[1] * sc;
+      v[6] = f[0] * sc;
+      v[7] = f[1] * sc;
+    } else if (j.fmt == IDX_K_MXFP4) {
+      const uint32_t w = *(const uint32_t *)(p + 4 * c);
+      const uint32_t e8 = s[c >> 2];
+      // E8M0 code 0 stands for 2^-127, a subnormal; 0xFF is NaN
+      const float sc = e8 == 0xFFu ? __uint_as_float(0x7FC00000u)
+                                   : __uint_as_float(e8 ? e8 << 23 : 0x00400000u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t q = w >> (4 * e);
+        const float y = E2M1_VALUE[q & 7u];
+        v[e] = (q & 8u ? -y : y) * sc;
+      }
+    } else {
+      values8(load8(p, j.fmt, 8 * c, 8 * c + 4, false), j.fmt, v);
+    }
+  }
+  uint8_t *o = j.out + (int64_t)t * j.out_t + (int64_t)h * j.out_h;
+  if (j.dtype == IDX_K_F32) {
+    *(float4 *)(o + 32 * c) = make_float4(v[0], v[1], v[2], v[3]);
+    *(float4 *)(o + 32 * c + 16) = make_float4(v[4], v[5], v[6], v[7]);
+  } else if (j.dtype == IDX_K_BF16) {
+    *(uint4 *)(o + 16 * c) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  } else {
+    *(uint4 *)(o + 16 * c) =
+        make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+  }
+}
+
+// Every pair of rows: quadratic, for debugging only.
+__global__ __launch_bounds__(THREADS) void slot_check_kernel(const int32_t *slot, int32_t T, int64_t rows,
+                                                             uint32_t *word) {
+  const int64_t t = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+  if (t >= T) return;
+  const int32_t s = slot[t];
+  if (s < 0 || s >= rows) return;
+  for (int64_t u = 0; u < t; ++u)
+    if (slot[u] == s) {
+      atomicOr(word, 32u);
+      return;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
+  int64_t blocks = 0;
+  int m = 0;
+  for (int i = 0; i < jobs.n; ++i) {
+    RowJob j = jobs.job[i];
+    if (j.T <= 0 || j.H <= 0 || j.rows <= 0) continue;
+    j.lanes_sh = 0;
+    while ((8 << j.lanes_sh) < j.D) ++j.lanes_sh;
+    j.groups = (j.H + HEADS - 1) / HEADS;
+    jobs.job[m] = j;
+    jobs.first[m++] = (int32_t)blocks;
+    const int per = THREADS >> j.lanes_sh;
+    blocks += ((int64_t)j.T * j.groups + per - 1) / per;
+    if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  }
+  jobs.n = m;
+  jobs.first[m] = (int32_t)blocks;
+  if (!m) return hipSuccess;
+  hipLaunchKernelGGL(write_kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, jobs);
+  return hipGetLastError();
+}
+
+hipError_t launch_read(const ReadJob &j, hipStream_t s) {
+  const int64_t total = (int64_t)j.T * j.H * (j.D / 8);
+  if (total <= 0) return hipSuccess;
+  const int64_t blocks = (total + THREADS - 1) / THREADS;
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(read_kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, j);
+  return hipGetLastError();
+}
+
+hipError_t launch_slot_check(const int32_t *slot, int32_t T, int64_t rows, uint32_t *word, hipStream_t s) {
+  if (T <= 0) return hipSuccess;
+  hipLaunchKernelGGL(slot_check_kernel, dim3((unsigned)((T + THREADS - 1) / THREADS)), dim3(THREADS), 0, s, slot, T,
+                     rows, word);
+  return hipGetLastError();
+}
+
+}  // namespace idx
