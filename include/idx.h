@@ -429,7 +429,7 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
  * twice.  Rows that do not count are not read, so what they hold reaches no output.  The order of
  * entries has no influence beyond the rounding of sums; results are bitwise repeatable.
  * q and out share type and sizes, IDX_K_BF16 or IDX_K_F16; the caches are of that type or E4M3, both
- * alike; D = 64 or 128.  Products run on the matrix cores with fp32 accumulation, E4M3 codes
+ * alike, with the same slots and strides; D = 64 or 128.  Products run on the matrix cores with fp32 accumulation, E4M3 codes
  * converted exactly; weights are rounded to 16 bits before the second product (2^-9 relative in
  * bf16, 2^-12 in fp16: bf16 wherever v is E4M3), sums and maxima are fp32.
  * ws: idx_sparse_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap

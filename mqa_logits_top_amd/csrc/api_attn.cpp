@@ -18,6 +18,8 @@ constexpr int32_t MAX_ROT = 512;
 constexpr int32_t MAX_POOL = 64;
 constexpr int64_t MAX_LD = (int64_t)1 << 31;   // strides: their products with 32-bit counts stay inside 64 bits
 
+constexpr int64_t MAX_ROW = (int64_t)1 << 30;  // elements of an attention cache's slot: 32 bits of bytes
+
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 idx_status launched(hipError_t e) { return e == hipSuccess ? IDX_OK : IDX_E_LAUNCH; }
 
@@ -127,6 +129,8 @@ idx_status check_attn(const idx_attn *a) {
   if (a->k.fmt != a->v.fmt) return IDX_E_FORMAT;
   if (a->k.fmt != a->q.dtype && a->k.fmt != IDX_K_FP8_E4M3) return IDX_E_UNSUPPORTED;
   if (a->q.D != 64 && a->q.D != 128) return IDX_E_UNSUPPORTED;
+  if (a->k.ld != a->v.ld || a->k.ld_scale != a->v.ld_scale) return IDX_E_SHAPE;
+  if (a->k.ld > MAX_ROW) return IDX_E_UNSUPPORTED;
   if (a->L < 0 || a->n_sel < 0 || a->ld_sel < 0 || (a->q.T > 1 && a->ld_sel < a->n_sel)) return IDX_E_SHAPE;
   if (!a->slot_of_key && a->L > a->k.rows) return IDX_E_SHAPE;
   if (a->pool < 1 || a->pool > MAX_POOL || (a->pool & (a->pool - 1))) return IDX_E_UNSUPPORTED;
@@ -280,12 +284,10 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
   g.out_h = 2 * a->out.ld_h;
   g.k = (const uint8_t *)a->k.data;
   g.v = (const uint8_t *)a->v.data;
-  g.k_t = bytes_of(a->k.ld, a->k.fmt);
-  g.v_t = bytes_of(a->v.ld, a->v.fmt);
+  g.row_bytes = (uint32_t)bytes_of(a->k.ld, a->k.fmt);
   g.k_scale = (const float *)a->k.scale;
   g.v_scale = (const float *)a->v.scale;
-  g.ks_t = a->k.ld_scale;
-  g.vs_t = a->v.ld_scale;
+  g.scale_row = a->k.ld_scale;
   g.rows = a->k.rows;
   g.sel = a->sel;
   g.ld_sel = a->ld_sel;

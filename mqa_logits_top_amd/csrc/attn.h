@@ -13,9 +13,9 @@ struct AttnArgs {
   uint8_t *out;
   int64_t out_t, out_h;
   const uint8_t *k, *v;
-  int64_t k_t, v_t;          // bytes of a slot; a head is D values on
+  uint32_t row_bytes;        // of a slot, in both caches; a head is D values on
   const float *k_scale, *v_scale;
-  int64_t ks_t, vs_t;        // floats of a slot
+  int64_t scale_row;         // floats of a slot
   int64_t rows;              // slots in both caches
   const int32_t *sel;
   int64_t ld_sel;
@@ -24,7 +24,8 @@ struct AttnArgs {
   const int32_t *table;
   int32_t L;
   int32_t T, Hq, Hkv, G;
-  float scale2;              // scale * log2(e)
+  float scale2;              // scale * log2(e); launch_attn makes it >= 0 ...
+  uint32_t q_sign;           // ... and flips q's signs instead (filled there)
   float *lse;
   int32_t blocks;            // head blocks of a cache head's G query heads
   int32_t splits;            // workgroups a row's entries are divided over

@@ -103,7 +103,8 @@ def test_attn_refusals(lib):
     for status, bad in [
             (SHAPE, dict(q=r(T=3))), (SHAPE, dict(out=r(H=8))), (SHAPE, dict(k=_cache(H=4))),
             (SHAPE, dict(k=_cache(H=5), v=_cache(H=5))), (SHAPE, dict(v=_cache(rows=99))),
-            (SHAPE, dict(k=_cache(D=64))), (SHAPE, dict(n_sel=-1)), (SHAPE, dict(ld_sel=639)), (SHAPE, dict(L=101)),
+            (SHAPE, dict(k=_cache(D=64))), (SHAPE, dict(k=_cache(ld=2048))), (SHAPE, dict(v=_cache(ld_scale=16))),
+            (UNSUPPORTED, dict(k=_cache(ld=2 ** 31), v=_cache(ld=2 ** 31))), (SHAPE, dict(n_sel=-1)), (SHAPE, dict(ld_sel=639)), (SHAPE, dict(L=101)),
             (SHAPE, dict(L=-1)), (FORMAT, dict(q=r(dtype=F32), out=r(dtype=F32))), (FORMAT, dict(out=r(dtype=F16))),
             (FORMAT, dict(k=_cache(fmt=BF16))), (UNSUPPORTED, dict(k=_cache(fmt=F16), v=_cache(fmt=F16))),
             (UNSUPPORTED, dict(k=_cache(fmt=FP4), v=_cache(fmt=FP4))),
@@ -111,7 +112,7 @@ def test_attn_refusals(lib):
             (UNSUPPORTED, dict(pool=3, ks=F, ke=F)), (UNSUPPORTED, dict(pool=0)), (UNSUPPORTED, dict(pool=128, ks=F, ke=F)),
             (PARAM, dict(scale=float("inf"))), (NULL, dict(ks=F)), (NULL, dict(pool=8)), (NULL, dict(sel=None)),
             (NULL, dict(q=r(data=None))), (ALIGN, dict(sel=F + 2)), (ALIGN, dict(lse=F + 1)),
-            (ALIGN, dict(v=_cache(ld=1032))), (ALIGN, dict(ks=F + 1, ke=F)), (ALIGN, dict(slot_of_key=F + 3)), (ALIGN, dict(q=r(data=F + 8)))]:
+            (ALIGN, dict(k=_cache(ld=1032), v=_cache(ld=1032))), (ALIGN, dict(ks=F + 1, ke=F)), (ALIGN, dict(slot_of_key=F + 3)), (ALIGN, dict(q=r(data=F + 8)))]:
         assert size(**bad) == status, bad
         assert lib.idx_sparse_attn(_attn(**bad), F, 1 << 30, None) == status, bad
     assert size(slot_of_key=F, L=1 << 20) == OK
