@@ -36,7 +36,7 @@ struct AttnArgs {
 };
 
 struct AttnPlan {
-  int32_t tiles;             // 16-head tiles a wave holds: 1, 2 or 4
+  int32_t tiles;             // 16-head tiles a wave holds: 1 or 2
   int32_t blocks;
   int32_t splits;
   size_t bytes;              // workspace

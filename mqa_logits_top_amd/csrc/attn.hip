@@ -1,17 +1,16 @@
 // Attention of each query row over the keys its list selects.
 //
-// A workgroup serves one row t, one cache head and up to 64 of its query heads.  Its four waves
-// take 32-key tiles of the list in turn, each with a softmax of its own (running maximum m, sum l
-// and unnormalised output O), joined through LDS at the end.  Keys and values go straight from
-// memory to the matrix cores' operand registers:
-//   S^T = K Q^T  (v_mfma 16x16x32): A = 16 keys x 32 dims, lane l holds key l % 16, 8 dims of group
-//     g = l / 16; the result gives lane l head l % 16 and keys 4 g .. 4 g + 3 of the tile.
-//   O^T += V^T P^T: B = P^T, lane l holds head l % 16 and 8 of the 32 keys.  The product sums over
-//     keys, so their order is free: taking keys 4g + j and 16 + 4g + j for group g makes the two S^T
-//     results, exponentiated, the operand as they stand.  A = V^T: lane l reads dims
-//     [c D/16, (c + 1) D/16), c = l % 16, of the same 8 keys (16 lanes read a whole row) and
-//     transposes 8 keys x D/16 dims in registers; tile n's row c is then dim c D/16 + n.
-// So no tile passes through LDS and no barrier stands in the loop.
+// A wave serves one row t, one cache head and 16 or 32 of its query heads, alone: no barrier, no join inside
+// a workgroup.  The list's entries that count go, without gaps, to a queue in LDS; a step takes 32 of them:
+//   S^T = K Q^T  (v_mfma 16x16x32, twice 16 keys): A = keys x 32 dims, lane l holds key l % 16 and 8 dims of
+//     group g = l / 16; the result gives lane l head l % 16 and keys 4 g .. 4 g + 3 of the 16.
+//   O^T += V^T P^T: B = P^T, lane l holds head l % 16 and 8 of the 32 keys.  The product sums over keys, so
+//     their order is free: with positions 8 g + 4 h + j for the keys 4 g + j of the h-th 16, the two S^T
+//     results, exponentiated, are the operand as they stand.  A = V^T comes transposed out of LDS.
+// The softmax is the running one: a reference near the maximum, the sum, the unnormalised output.
+// Cache rows reach LDS by memory-to-LDS copies that each bring whole rows, K for the next step while this one
+// multiplies, V while the next one's scores are computed.  Waves of the 2000 rows that are resident at once
+// walk their ascending lists at the same pace, so each XCD's L2 meets a row's neighbours' keys soon after.
 #include "attn.h"
 
 #include <cmath>
@@ -31,6 +30,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+typedef int16_t i16x4 __attribute__((ext_vector_type(4)));
 
 template <bool BF16>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -82,10 +83,38 @@ __device__ __forceinline__ float head_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+__device__ __forceinline__ float max8(const float *x) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __builtin_fmaxf(m, x[i]);
+  return m;
+}
+
 // Lanes of the wave exchange data through LDS: its accesses complete in order, the compiler must not move them.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+// Memory-to-LDS copies: lane l's 16 (4) bytes land at LDS byte lds + 16 l (4 l); lds is wave-uniform and goes
+// through m0, which nothing else here uses.  The compiler does not count them, so the kernel waits itself:
+// copies and loads of a wave complete in the order of their issue, so with at most N operations under way
+// every copy is there that N others certainly followed; more of them only make the wait stricter.
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+__device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(const lds_u8 *)p; }
+__device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(const uint8_t *base, uint64_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(base + off), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(const float *p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 // Every LDS read so far has its data: the memory they read may be written by a copy.
 __device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -99,16 +128,18 @@ __device__ __forceinline__ float lse_of(float ref, float l) {
 // BF16: q's type; FP8: E4M3 caches (else of q's type); MT: 16-head tiles.
 // WIDE: caches past 2^32 bytes (64-bit offsets of rows instead of 32-bit ones beside a uniform base).
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
-__global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64, 2) void attn_kernel(AttnArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
   constexpr int KS = D / 32;              // steps of the first product
-  constexpr int DN = D / 16;              // dims of a lane's V piece, and tiles of the second product
+  constexpr int DN = D / 16;              // tiles of the second product
   constexpr int HEADS = MT * 16;
   constexpr int RB = FP8 ? D : 2 * D;     // bytes of a cache row
   constexpr int CH = RB / 16;             // its 16-byte chunks
-  constexpr int NI = CH / 2;              // copies of a tile's K: 64 / CH rows each
+  constexpr int NI = CH / 2;              // copies of a tile's K or V: 64 / CH rows each
   constexpr int PER = 16 / CH;            // rows a 16-lane group brings in one copy
+  constexpr int NK = NI + (FP8 ? 1 : 0);  // copies of a tile's K and scales
   __shared__ __attribute__((aligned(16))) uint8_t kbuf[TILE * RB];
+  __shared__ __attribute__((aligned(16))) uint8_t vbuf[TILE * RB];
   __shared__ __attribute__((aligned(16))) uint32_t queue[QUEUE];
   __shared__ __attribute__((aligned(16))) uint32_t offsets[WIDE ? 1 : QUEUE];   // the queue's rows in bytes
   __shared__ __attribute__((aligned(16))) float scales[FP8 ? 2 * TILE : 1];
@@ -116,13 +147,13 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
 
   const int lane = threadIdx.x;
   const int c = lane & 15, g = lane >> 4;
-  int64_t item = blockIdx.x;
-  const int split = (int)(item % a.splits);
-  item /= a.splits;
-  const int hb = (int)(item % a.blocks);
-  item /= a.blocks;
-  const int kvh = (int)(item % a.Hkv);
-  const int t = (int)(item / a.Hkv);
+  uint32_t item = blockIdx.x;
+  const int split = (int)(item % (uint32_t)a.splits);
+  item /= (uint32_t)a.splits;
+  const int hb = (int)(item % (uint32_t)a.blocks);
+  item /= (uint32_t)a.blocks;
+  const int kvh = (int)(item % (uint32_t)a.Hkv);
+  const int t = (int)(item / (uint32_t)a.Hkv);
   const int head0 = kvh * a.G + hb * HEADS;                    // first query head
   const int heads = min(HEADS, a.G - hb * HEADS);
 
@@ -133,29 +164,34 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
   const int64_t e_end = min(entries, (split + 1) * per);
   int64_t e_next = split * per;           // first entry whose id is not loaded
   const int32_t *list = a.sel + (int64_t)t * a.ld_sel;
-  int32_t key[4], row[4];                 // the chunk after next: keys; the next chunk: rows
-  auto load_keys = [&] {
+  // Three chunks are under way: the one that fill() appends (row), whose slots are loading (row, once it
+  // is appended), and the one behind it, whose ids are loading (id).  Nothing waits for a load just issued.
+  int32_t id[4], row[4];
+  auto load_ids = [&] {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int64_t e = e_next + 64 * r + lane;
-      int64_t k = -1;
-      if (e < e_end) {
-        const int32_t id = list[e >> a.pool_sh];
-        k = id;
-        if (a.pool_sh && id >= 0) k = (int64_t)win0 + ((int64_t)id << a.pool_sh) + (e & ((1 << a.pool_sh) - 1));
-      }
-      key[r] = k >= win0 && k < win1 ? (int32_t)k : -1;
-    }
+    for (int r = 0; r < 4; ++r) id[r] = list[min(e_next + 64 * r + lane, e_end - 1) >> a.pool_sh];
     e_next += CHUNK;
   };
-  auto load_rows = [&] {
+  auto load_rows = [&] {   // of the ids loaded last
 #pragma unroll
-    for (int r = 0; r < 4; ++r) row[r] = a.table && key[r] >= 0 ? a.table[key[r]] : key[r];
+    for (int r = 0; r < 4; ++r) {
+      const int64_t e = e_next - CHUNK + 64 * r + lane;
+      int64_t key = id[r];
+      if (a.pool_sh) key = (key << a.pool_sh) + win0 + (e & ((1 << a.pool_sh) - 1));
+      const bool ok = e < e_end && id[r] >= 0 && key >= win0 && key < win1;
+      row[r] = ok ? (int32_t)key : -1;
+      if (a.table && ok) row[r] = a.table[key];
+    }
   };
   int64_t e_left = e_end - e_next;        // entries not in the queue yet
-  uint32_t head = 0, tail = 0;            // queue positions (modulo QUEUE); entries in order, no gaps
+  // the queue holds positions [head, tail): entries that count, in order, no gaps; head is the current
+  // tile's first, a multiple of TILE
+  uint32_t head = 0, tail = 0;
+  // Makes the tile after the current one whole, if the list has that much left; behind the list's last
+  // entry the last tile repeats it.
   auto fill = [&] {
-    while (tail - head < 2 * TILE && e_left > 0) {
+    if (tail - head >= 2 * TILE || e_left <= 0) return;
+    do {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const bool ok = row[r] >= 0 && row[r] < a.rows;
@@ -170,15 +206,23 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
       e_left -= CHUNK;
       if (e_left > 0) {
         load_rows();
-        if (e_left > CHUNK) load_keys();
+        if (e_left > CHUNK) load_ids();
       }
-    }
+    } while (tail - head < 2 * TILE && e_left > 0);
     wave_sync();
+    if (e_left <= 0 && (tail & (TILE - 1))) {
+      const uint32_t last = (tail - 1) & (QUEUE - 1), at = tail + (uint32_t)lane;
+      if (at < ((tail + TILE - 1) & ~(uint32_t)(TILE - 1))) {
+        if constexpr (WIDE || FP8) queue[at & (QUEUE - 1)] = queue[last];
+        if constexpr (!WIDE) offsets[at & (QUEUE - 1)] = offsets[last];
+      }
+      wave_sync();
+    }
   };
   if (e_left > 0) {
-    load_keys();
+    load_ids();
     load_rows();
-    if (e_left > CHUNK) load_keys();
+    if (e_left > CHUNK) load_ids();
   }
 
   // Q^T as B operands: lane l holds head l % 16 and the dims its K piece holds in that step
@@ -195,10 +239,11 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
     }
 
   f32x4 o[MT][DN];
-  float ref[MT], sum[MT];
+  float ref[MT], neg[MT], sum[MT];        // neg: -ref, or 0 while there is none
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     ref[m] = NEG_INF;
+    neg[m] = 0.f;
     sum[m] = 0.f;
 #pragma unroll
     for (int n = 0; n < DN; ++n) o[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -206,97 +251,95 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
 
   const uint8_t *kbase = a.k + (int64_t)RB * kvh, *vbase = a.v + (int64_t)RB * kvh;
   const float *sbase = (lane < TILE ? a.k_scale : a.v_scale) + kvh;
-  // K copy u brings position 8 g + PER u + c / CH of the tile to LDS row u 4 PER + lane / CH, chunks swizzled
-  // so that 16 lanes reading one chunk of 16 rows meet every bank once
-  auto ldsrow = [](int p) { return (p & 7) / PER * 4 * PER + (p >> 3) * PER + (p & 7) % PER; };
-  auto swizzle = [](int r) { return (r / PER) & (CH - 1); };
+  // Copy u brings position 8 g + e, e = PER u + c / CH, of the tile to LDS row u 4 PER + lane / CH, its chunks
+  // exchanged (xor) so that lanes that read together meet different banks.  K: 16 lanes read one chunk of 16
+  // rows, in passes that mix lanes 0-3, 12-15 of one group with 4-11 of the next.  V: a pass of 32 lanes reads
+  // 32 bytes of 8 rows, or 16 bytes (E4M3) of 16.
+  auto ldsrow = [](int g, int e) { return e / PER * 4 * PER + g * PER + e % PER; };
+  auto swizzle_k = [](int g, int e) {
+    return CH == 16 ? (g << 2) | (e & 3) : CH == 8 ? (g << 1) | ((e >> 1) & 1) : (g & 1) * 3;
+  };
+  auto swizzle_v = [](int g, int e) {
+    if constexpr (FP8) return (e / PER << 1) | (g & 1);
+    return ((CH == 16 ? e & 3 : (e >> 1) & 1) << 2) | ((g & 1) << 1) | (g >> 1);
+  };
   Off off[8];                             // of the lane's 8 positions 8 g .. 8 g + 7
-  float scale_in = 0.f;
-  uint32_t vr[8][DN / 2];                 // V: DN dims of them (E4M3: their codes in the first words)
+  uint32_t scale_row = 0;                 // E4M3: of position lane % 32
 
+  auto copy_row = [&](int u) -> Off {
+    Off b = off[PER * u];
+    if constexpr (PER > 1) {
+      const Off b1 = off[PER * u + 1];
+      b = c / CH == 1 ? b1 : b;
+    }
+    if constexpr (PER > 2) {
+      const Off b2 = off[PER * u + 2], b3 = off[PER * u + 3];
+      b = c / CH == 2 ? b2 : c / CH == 3 ? b3 : b;
+    }
+    return b;
+  };
   auto request_k = [&] {
 #pragma unroll
-    for (int u = 0; u < NI; ++u) {
-      Off b = off[PER * u];
-      if constexpr (PER > 1) {
-        const Off b1 = off[PER * u + 1];
-        b = c / CH == 1 ? b1 : b;
-      }
-      if constexpr (PER > 2) {
-        const Off b2 = off[PER * u + 2], b3 = off[PER * u + 3];
-        b = c / CH == 2 ? b2 : c / CH == 3 ? b3 : b;
-      }
-      const int r = u * 4 * PER + lane / CH;
-      const uint8_t *p = kbase + (Off)(b + (((lane & (CH - 1)) ^ swizzle(r)) << 4));
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)p,
-                                       (__attribute__((address_space(3))) void *)(kbuf + u * 1024), 16, 0, 0);
-    }
+    for (int u = 0; u < NI; ++u)
+      copy16(kbase, (Off)(copy_row(u) + (((lane & (CH - 1)) ^ swizzle_k(g, PER * u + c / CH)) << 4)),
+             lds_addr(kbuf) + u * 1024);
+    // lanes 0 .. 31 bring their key's scale, the others their value's
+    if constexpr (FP8) copy4(sbase + (int64_t)scale_row * a.scale_row, lds_addr(scales));
   };
   auto request_v = [&] {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint8_t *p = vbase + (Off)(off[i] + (RB / 16) * c);
-      if constexpr (RB == 256)
-        *(u32x4 *)vr[i] = *(const u32x4 *)p;
-      else if constexpr (RB == 128)
-        *(uint2 *)vr[i] = *(const uint2 *)p;
-      else
-        vr[i][0] = *(const uint32_t *)p;
-    }
+    for (int u = 0; u < NI; ++u)
+      copy16(vbase, (Off)(copy_row(u) + (((lane & (CH - 1)) ^ swizzle_v(g, PER * u + c / CH)) << 4)),
+             lds_addr(vbuf) + u * 1024);
   };
-  // the next tile's addresses, from the queue; returns how many of its positions count
-  auto next_tile = [&]() -> int {
-    fill();
-    const int n = min((int)(tail - head), TILE);
-    if (n > 0) {
+  // addresses of the tile at queue position `at`; spread 0: of its first rows only, over and over
+  auto next_tile = [&](uint32_t at, int spread) {
+    at &= QUEUE - 1;
+    const u32x4 lo = *(const u32x4 *)&(WIDE ? queue : offsets)[at + (8 * g & spread)];
+    const u32x4 hi = *(const u32x4 *)&(WIDE ? queue : offsets)[at + (8 * g & spread) + 4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t at = (head + (uint32_t)min(8 * g + i, n - 1)) & (QUEUE - 1);
-        off[i] = WIDE ? (Off)queue[at] * a.row_bytes : (Off)offsets[at];
-      }
-      if constexpr (FP8) {
-        const uint32_t r = queue[(head + (uint32_t)min(lane & (TILE - 1), n - 1)) & (QUEUE - 1)];
-        scale_in = sbase[(int64_t)r * a.scale_row];
-      }
+    for (int i = 0; i < 8; ++i) {
+      off[i] = i < 4 ? lo[i & 3] : hi[i & 3];
+      if constexpr (WIDE) off[i] *= a.row_bytes;
     }
-    head += (uint32_t)n;
-    return n;
+    if constexpr (FP8) scale_row = queue[at + (lane & (TILE - 1) & spread)];
   };
 
-  int n = next_tile();
-  if (n > 0) {
+  fill();
+  bool more = tail != 0;
+  if (more) {
+    next_tile(0, -1);
     request_k();
     request_v();
   }
-  while (n > 0) {
-    // this tile's K from LDS into operands, then the copy of the next tile's may start
+  for (; more; head += TILE) {
+    copies_left<NI>();   // this tile's K is there (its V followed)
+    fill();
+    // the list's last tile may be partial; the others are whole
+    const int n = (int)(tail - head);
+    more = n > TILE;
+    // K from LDS into operands, then the copy of the next tile's may start
     u32x4 kt[2][KS];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = ldsrow(8 * (c >> 2) + 4 * h + (c & 3));
-      const uint8_t *p = kbuf + r * RB;
-      if constexpr (FP8) {
+      const int kg = c >> 2, ke = 4 * h + (c & 3);   // the position of key c of the h-th 16
+      const uint8_t *p = kbuf + ldsrow(kg, ke) * RB;
 #pragma unroll
-        for (int s = 0; s < KS; s += 2) kt[h][s] = *(const u32x4 *)(p + (((2 * s + g) ^ swizzle(r)) << 4));
-      } else {
-#pragma unroll
-        for (int s = 0; s < KS; ++s) kt[h][s] = *(const u32x4 *)(p + (((4 * s + g) ^ swizzle(r)) << 4));
-      }
+      for (int s = 0; s < KS; s += FP8 ? 2 : 1)
+        kt[h][s] = *(const u32x4 *)(p + ((((FP8 ? 2 : 4) * s + g) ^ swizzle_k(kg, ke)) << 4));
     }
     float ksc[8], vsc[8];
     if constexpr (FP8) {
-      scales[lane] = scale_in;
-      wave_sync();
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         ksc[i] = scales[8 * g + i] * a.scale2;
-        vsc[i] = 8 * g + i < n ? scales[TILE + 8 * g + i] : 0.f;
+        vsc[i] = scales[TILE + 8 * g + i];
       }
     }
-    const int now_n = n;
-    n = next_tile();
+    // behind the last tile its first rows are requested once more and not used: the waits count on it
+    next_tile(more ? head + TILE : head, more ? -1 : 0);
     lds_done();
-    if (n > 0) request_k();
+    request_k();
     if constexpr (FP8) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -310,48 +353,53 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
         }
     }
 
-    u32x4 p[MT];
+    float sc[MT][8];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float sc[8];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < KS; ++s) acc = mfma<BF16>(kt[h][s], q[m][s], acc);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sc[4 * h + j] = FP8 ? acc[j] * ksc[4 * h + j] : acc[j];
+        for (int j = 0; j < 4; ++j) {
+          const int i = 4 * h + j;
+          sc[m][i] = FP8 ? acc[j] * ksc[i] : acc[j];
+        }
       }
-      if (now_n < TILE) {
+    if (!more) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (8 * g + i >= now_n) sc[i] = NEG_INF;
-      }
-      float top = sc[0];
+          if (8 * g + i >= n) sc[m][i] = NEG_INF;
+    }
+    u32x4 p[MT];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, sc[i]);
+    for (int m = 0; m < MT; ++m) {
+      float top = max8(sc[m]);
       if constexpr (!FP8) top *= a.scale2;     // scale2 >= 0: the largest product is the largest dot's
-      const float now = head_max(top);
-      // the reference moves only when a score is 2^8 above it: weights then stay below 2^8, and the
-      // accumulators are rescaled a few times a row instead of at most tiles
-      if (__any(now > ref[m] + 8.f)) {
-        const float to = __builtin_fmaxf(ref[m], now);
+      // The reference moves only when a score is 2^8 above it: weights then stay below 2^8, and the
+      // accumulators are rescaled a few times a row instead of at most tiles.  The four lanes of a head
+      // share their reference, so a lane's own scores decide whether there is anything to do.
+      if (__any(top > ref[m] + 8.f)) {
+        const float to = __builtin_fmaxf(ref[m], head_max(top));
         const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
         sum[m] *= f;
 #pragma unroll
-        for (int n2 = 0; n2 < DN; ++n2) o[m][n2] *= f;
+        for (int d = 0; d < DN; ++d) o[m][d] *= f;
         ref[m] = to;
+        neg[m] = to == NEG_INF ? 0.f : -to;
       }
-      const float base = ref[m] == NEG_INF ? 0.f : ref[m];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float x, y;
         if constexpr (FP8) {
-          x = __builtin_amdgcn_exp2f(sc[2 * i] - base);
-          y = __builtin_amdgcn_exp2f(sc[2 * i + 1] - base);
+          x = __builtin_amdgcn_exp2f(sc[m][2 * i] + neg[m]);
+          y = __builtin_amdgcn_exp2f(sc[m][2 * i + 1] + neg[m]);
         } else {
-          x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i], a.scale2, -base));
-          y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i + 1], a.scale2, -base));
+          x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[m][2 * i], a.scale2, neg[m]));
+          y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[m][2 * i + 1], a.scale2, neg[m]));
         }
         sum[m] += x + y;
         if constexpr (FP8) {
@@ -362,46 +410,62 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
       }
     }
 
-    // V^T operands: vt[d] packs the 8 keys of dim c DN + d
-    if (now_n < TILE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (8 * g + i >= now_n) {
-#pragma unroll
-          for (int x = 0; x < DN / 2; ++x) vr[i][x] = 0u;
-        }
-    }
+    // V^T operands: the 8 keys 8 g .. 8 g + 7 of dim 16 d + c
+    copies_left<NK>();   // this tile's V is there (the next one's K followed)
     u32x4 vt[DN];
     if constexpr (FP8) {
+      // transposed 8 keys x 16 dims of a group: lane 2 r + x points to key r, dims 8 x .. 8 x + 7
+      const uint8_t *p = vbuf + ldsrow(g, c >> 1) * RB + 8 * (c & 1);
 #pragma unroll
-      for (int x = 0; x < DN / 4; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint32_t e = vr[2 * y][x], f = vr[2 * y + 1][x];
-          const uint32_t lo0 = codes2<true, false>(e), lo1 = codes2<true, false>(f);
-          const uint32_t hi0 = codes2<true, true>(e), hi1 = codes2<true, true>(f);
-          vt[4 * x][y] = __builtin_amdgcn_perm(lo1, lo0, 0x05040100u);
-          vt[4 * x + 1][y] = __builtin_amdgcn_perm(lo1, lo0, 0x07060302u);
-          vt[4 * x + 2][y] = __builtin_amdgcn_perm(hi1, hi0, 0x05040100u);
-          vt[4 * x + 3][y] = __builtin_amdgcn_perm(hi1, hi0, 0x07060302u);
-        }
+      for (int d = 0; d < DN; ++d) {
+        const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2 *)(p + ((d ^ swizzle_v(g, c >> 1)) << 4)));
+        vt[d][0] = (uint32_t)w[0];
+        vt[d][1] = (uint32_t)w[1];
+      }
     } else {
+      // transposed 4 keys x 16 dims: lane 4 r + x points to key r, dims 4 x .. 4 x + 3
 #pragma unroll
-      for (int x = 0; x < DN / 2; ++x)
+      for (int h = 0; h < 2; ++h) {
+        const int ve = 4 * h + (c >> 2);
+        const uint8_t *p = vbuf + ldsrow(g, ve) * RB + 8 * (c & 1);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          vt[2 * x][y] = __builtin_amdgcn_perm(vr[2 * y + 1][x], vr[2 * y][x], 0x05040100u);
-          vt[2 * x + 1][y] = __builtin_amdgcn_perm(vr[2 * y + 1][x], vr[2 * y][x], 0x07060302u);
+        for (int d = 0; d < DN; ++d) {
+          const i32x2 w = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) i16x4 *)(p + (((2 * d + ((c & 3) >> 1)) ^ swizzle_v(g, ve)) << 4))));
+          vt[d][2 * h] = (uint32_t)w[0];
+          vt[d][2 * h + 1] = (uint32_t)w[1];
         }
+      }
     }
-    if (n > 0) request_v();
+    lds_done();
+    request_v();
+    if (!more) {   // keys behind the list's end are zeros
+      const int left = n - 8 * g;
+#pragma unroll
+      for (int y = 0; y < (FP8 ? 2 : 4); ++y) {
+        constexpr int PACK = FP8 ? 4 : 2, BITS = FP8 ? 8 : 16;   // keys of a word
+        const int keys = min(max(left - PACK * y, 0), PACK);
+        const uint32_t keep = keys == PACK ? ~0u : (1u << (keys * BITS)) - 1u;
+#pragma unroll
+        for (int d = 0; d < DN; ++d) vt[d][y] &= keep;
+      }
+    }
+    if constexpr (FP8) {
+#pragma unroll
+      for (int d = 0; d < DN; ++d)
+        vt[d] = u32x4{codes2<true, false>(vt[d][0]), codes2<true, true>(vt[d][0]), codes2<true, false>(vt[d][1]),
+                      codes2<true, true>(vt[d][1])};
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int d = 0; d < DN; ++d) o[m][d] = mfma<PV_BF16>(vt[d], p[m], o[m][d]);
   }
 
-  // lane l holds head l % 16 and dims (4 g + j) DN + d
+  copies_left<0>();   // none may write LDS that is another wave's by then
+
+  // lane l holds head l % 16 and dims 16 d + 4 g + j
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const float l = head_sum(sum[m]);
@@ -414,21 +478,14 @@ __global__ __launch_bounds__(64, MT == 4 ? 1 : 2) void attn_kernel(AttnArgs a) {
         a.part_ml[2 * at + 1] = l;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int d = 0; d < DN; d += 4)
-          *(f32x4 *)(a.part + at * D + (4 * g + j) * DN + d) =
-              f32x4{o[m][d][j], o[m][d + 1][j], o[m][d + 2][j], o[m][d + 3][j]};
+      for (int d = 0; d < DN; ++d) *(f32x4 *)(a.part + at * D + 16 * d + 4 * g) = o[m][d];
     } else {
       const float f = finish(l);
       uint8_t *dst = a.out + (int64_t)t * a.out_t + (int64_t)(head0 + h) * a.out_h;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int d = 0; d < DN; d += 4)
-          *(uint2 *)(dst + 2 * ((4 * g + j) * DN + d)) =
-              make_uint2(pack2<BF16>(o[m][d][j] * f, o[m][d + 1][j] * f),
-                         pack2<BF16>(o[m][d + 2][j] * f, o[m][d + 3][j] * f));
+      for (int d = 0; d < DN; ++d)
+        *(uint2 *)(dst + 2 * (16 * d + 4 * g)) =
+            make_uint2(pack2<BF16>(o[m][d][0] * f, o[m][d][1] * f), pack2<BF16>(o[m][d][2] * f, o[m][d][3] * f));
       if (g == 0 && a.lse) a.lse[(int64_t)t * a.Hq + head0 + h] = lse_of(ref[m], l);
     }
   }
@@ -489,9 +546,7 @@ hipError_t launch_one(const AttnArgs &a, unsigned blocks, hipStream_t s) {
 }
 template <bool BF16, bool FP8, int D>
 hipError_t launch_tiles(const AttnArgs &a, int tiles, unsigned blocks, hipStream_t s) {
-  if (tiles == 1) return launch_one<BF16, FP8, D, 1>(a, blocks, s);
-  if (tiles == 2) return launch_one<BF16, FP8, D, 2>(a, blocks, s);
-  return launch_one<BF16, FP8, D, 4>(a, blocks, s);
+  return tiles == 1 ? launch_one<BF16, FP8, D, 1>(a, blocks, s) : launch_one<BF16, FP8, D, 2>(a, blocks, s);
 }
 template <bool BF16, bool FP8>
 hipError_t launch_dim(const AttnArgs &a, int D, int tiles, unsigned blocks, hipStream_t s) {
@@ -502,7 +557,7 @@ hipError_t launch_dim(const AttnArgs &a, int D, int tiles, unsigned blocks, hipS
 
 AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries) {
   AttnPlan p{};
-  p.tiles = G <= 16 ? 1 : G <= 32 ? 2 : 4;
+  p.tiles = G <= 16 ? 1 : 2;
   int64_t items = 0;
   for (;; p.tiles /= 2) {
     const int32_t heads = 16 * p.tiles;
