@@ -9,11 +9,12 @@
 namespace idx {
 namespace {
 
-constexpr int HEADS = 4;       // heads a lane takes of one token: they share the sines and cosines
+constexpr int HEADS = 4;       // heads a lane takes of one token at most: they share the sines and cosines
 constexpr int THREADS = 256;
 
-struct Raw {
-  uint4 a, b;   // 8 elements: 16 bytes in a, or 32 bytes in a and b (fp32)
+template <bool F32>
+struct Raw {   // 8 elements
+  uint4 w[F32 ? 2 : 1];
 };
 
 __device__ __forceinline__ float bf16_val(uint32_t u) { return __uint_as_float(u << 16); }
@@ -48,35 +49,40 @@ __device__ __forceinline__ void unpack4(uint32_t w0, uint32_t w1, int dtype, flo
 
 // The lane's 8 elements: two groups of four at element offsets e0 and e1 (e1 = e0 + 4 unless the
 // lane holds both halves of four rotated pairs).
-__device__ __forceinline__ Raw load8(const uint8_t *p, int dtype, int e0, int e1, bool split) {
-  Raw r;
-  if (dtype == IDX_K_F32) {
-    r.a = *(const uint4 *)(p + 4 * e0);
-    r.b = *(const uint4 *)(p + 4 * e1);
-  } else if (split) {
+template <bool F32>
+__device__ __forceinline__ Raw<F32> load8(const uint8_t *p, int dtype, int e0, int e1, bool split) {
+  Raw<F32> r;
+  if constexpr (F32) {
+    if (dtype == IDX_K_F32) {
+      r.w[0] = *(const uint4 *)(p + 4 * e0);
+      r.w[1] = *(const uint4 *)(p + 4 * e1);
+      return r;
+    }
+  }
+  if (split) {
     const uint2 lo = *(const uint2 *)(p + 2 * e0), hi = *(const uint2 *)(p + 2 * e1);
-    r.a = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    r.b = make_uint4(0u, 0u, 0u, 0u);
+    r.w[0] = make_uint4(lo.x, lo.y, hi.x, hi.y);
   } else {
-    r.a = *(const uint4 *)(p + 2 * e0);
-    r.b = make_uint4(0u, 0u, 0u, 0u);
+    r.w[0] = *(const uint4 *)(p + 2 * e0);
   }
   return r;
 }
-__device__ __forceinline__ void values8(const Raw &r, int dtype, float *v) {
-  if (dtype == IDX_K_F32) {
-    v[0] = __uint_as_float(r.a.x);
-    v[1] = __uint_as_float(r.a.y);
-    v[2] = __uint_as_float(r.a.z);
-    v[3] = __uint_as_float(r.a.w);
-    v[4] = __uint_as_float(r.b.x);
-    v[5] = __uint_as_float(r.b.y);
-    v[6] = __uint_as_float(r.b.z);
-    v[7] = __uint_as_float(r.b.w);
-  } else {
-    unpack4(r.a.x, r.a.y, dtype, v);
-    unpack4(r.a.z, r.a.w, dtype, v + 4);
+template <bool F32>
+__device__ __forceinline__ void values8(const Raw<F32> &r, int dtype, float *v) {
+  if constexpr (F32) {
+    if (dtype == IDX_K_F32) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.w[i].x);
+        v[4 * i + 1] = __uint_as_float(r.w[i].y);
+        v[4 * i + 2] = __uint_as_float(r.w[i].z);
+        v[4 * i + 3] = __uint_as_float(r.w[i].w);
+      }
+      return;
+    }
   }
+  unpack4(r.w[0].x, r.w[0].y, dtype, v);
+  unpack4(r.w[0].z, r.w[0].w, dtype, v + 4);
 }
 
 // Largest of x over aligned groups of 2^sh lanes.
@@ -103,27 +109,67 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *v) {
   return (uint32_t)w;
 }
 
-// E2M1 code of |a| (ties to the even code), sign from x.
-__device__ __forceinline__ uint32_t e2m1(float x) {
-  const float a = __builtin_fabsf(x);
-  const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-  return c | (x < 0.f ? 8u : 0u);
+// Sine and cosine of an angle below 2^32, within a few 2^-50: the angle less its nearest multiple of pi/2
+// (pi/2 in three parts of 53 bits; each fma is exact but for its one rounding, and the angle's multiple k of
+// pi/2 is below 2^32), then the Taylor series of sine and cosine on [-pi/4, pi/4] (terms dropped: below
+// 2^-45 of 1) and the quadrant's exchange of the two.  No branch, a quarter of the library function's
+// instructions, which took more time than the rotation.
+__device__ __forceinline__ void sin_cos(double x, double *sn, double *cs) {
+  const double k = __builtin_rint(x * 0.63661977236758134308);   // 2 / pi
+  double r = __builtin_fma(-k, 1.57079632679489655800, x);
+  r = __builtin_fma(-k, 6.12323399573676603587e-17, r);
+  r = __builtin_fma(-k, -1.49738490485916983280e-33, r);
+  const double z = r * r;
+  double s = 1.0 / 6227020800.0;
+  s = __builtin_fma(s, z, -1.0 / 39916800.0);
+  s = __builtin_fma(s, z, 1.0 / 362880.0);
+  s = __builtin_fma(s, z, -1.0 / 5040.0);
+  s = __builtin_fma(s, z, 1.0 / 120.0);
+  s = __builtin_fma(s, z, -1.0 / 6.0);
+  s = __builtin_fma(s * z, r, r);
+  double c = -1.0 / 87178291200.0;
+  c = __builtin_fma(c, z, 1.0 / 479001600.0);
+  c = __builtin_fma(c, z, -1.0 / 3628800.0);
+  c = __builtin_fma(c, z, 1.0 / 40320.0);
+  c = __builtin_fma(c, z, -1.0 / 720.0);
+  c = __builtin_fma(c, z, 1.0 / 24.0);
+  c = __builtin_fma(c, z, -0.5);
+  c = __builtin_fma(c, z, 1.0);
+  const uint32_t q = (uint32_t)(int32_t)__builtin_fma(-4.0, __builtin_floor(k * 0.25), k);   // k modulo 4
+  const double a = q & 1u ? c : s, b = q & 1u ? s : c;
+  *sn = q & 2u ? -a : a;
+  *cs = (q + 1u) & 2u ? -b : b;
+}
+
+// The lane's four pairs: (v[e], v[4 + e]) for split halves, else neighbours.  In fp64 the products of the
+// fp32 factors are exact, so each result is rounded once.
+template <bool SPLIT>
+__device__ __forceinline__ void rotate4(float *v, const double *cs, const double *sn) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float &x = v[SPLIT ? e : 2 * e], &y = v[SPLIT ? 4 + e : 2 * e + 1];
+    const double a = x, b = y;
+    x = (float)(a * cs[e] - b * sn[e]);
+    y = (float)(b * cs[e] + a * sn[e]);
+  }
 }
 
 constexpr uint32_t TINY = 0x0D800000u;   // bits of 2^-100
 constexpr uint32_t INF = 0x7F800000u;
 
+// F32: some array of the call holds or receives fp32 values.
+template <bool F32>
 __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
   int ji = 0;
   while (ji + 1 < jobs.n && (int)blockIdx.x >= jobs.first[ji + 1]) ++ji;
   const RowJob &j = jobs.job[ji];
   const int sh = j.lanes_sh;
-  const int64_t unit = ((int64_t)((int)blockIdx.x - jobs.first[ji]) * THREADS + threadIdx.x) >> sh;
+  const uint32_t unit = ((blockIdx.x - (uint32_t)jobs.first[ji]) << (8 - sh)) + (threadIdx.x >> sh);
   const int c = threadIdx.x & ((1 << sh) - 1);
-  const int64_t t64 = unit / j.groups;
-  const int hs = (int)(unit - t64 * j.groups);
-  if (t64 >= j.T) return;        // whole lane groups leave together
-  const int t = (int)t64;
+  const uint32_t tu = unit / (uint32_t)j.groups;
+  const int hs = (int)(unit - tu * (uint32_t)j.groups);
+  if (tu >= (uint32_t)j.T) return;        // whole lane groups leave together
+  const int t = (int)tu;
   const bool live = c * 8 < j.D;
   const int64_t slot = j.slot ? (int64_t)j.slot[t] : (int64_t)t;
   if (slot < 0 || slot >= j.rows) return;
@@ -137,59 +183,88 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
     e0 = j.rot0 + part / 2;
     e1 = e0 + j.rot / 2;
   }
-  Raw raw[HEADS];
+  Raw<F32> raw[HEADS];
   const uint8_t *xt = j.x + (int64_t)t * j.x_t;
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
     const int h = hs + i * j.groups;
-    if (live && h < j.H) raw[i] = load8(xt + (int64_t)h * j.x_h, j.dtype, e0, e1, split);
+    if (live && h < j.H) raw[i] = load8<F32>(xt + (int64_t)h * j.x_h, j.dtype, e0, e1, split);
   }
-  float cs[4], sn[4];
+  double cs[4], sn[4];           // rounded to fp32
   if (turned) {
-    const double p = (double)j.pos[t];
+    const double p = (double)j.pos[t], gain_s = j.inverse ? -j.mscale : j.mscale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       double s, k;
-      sincos(p * j.freq[part / 2 + i], &s, &k);
-      cs[i] = (float)(k * j.mscale);
-      sn[i] = (float)(s * j.mscale);
-      if (j.inverse) sn[i] = -sn[i];
+      sin_cos(p * j.freq[part / 2 + i], &s, &k);
+      cs[i] = (double)(float)(k * j.mscale);
+      sn[i] = (double)(float)(s * gain_s);
     }
   }
+  float v[HEADS][8];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i) {
-    const int h = hs + i * j.groups;
-    if (h >= j.H) break;         // the same for the whole lane group
-    float v[8];
+    if (hs + i * j.groups >= j.H) break;         // the same for the whole lane group
     if (live) {
-      values8(raw[i], j.dtype, v);
+      values8<F32>(raw[i], j.dtype, v[i]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
     }
-    if (turned) {
+    if (j.half) {
+      if (turned) rotate4<true>(v[i], cs, sn);
+    } else {
+      if (turned) rotate4<false>(v[i], cs, sn);
+    }
+  }
+  uint8_t *const out = j.out + slot * j.out_t;
+
+  if (j.fmt == IDX_K_FP8_E4M3) {
+    // Lane 4 n + i of a group divides for head i (lanes_sh >= 2; else every lane for each): two divisions for
+    // all heads instead of two a head
+    uint32_t m[HEADS];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // fp64: the fp32 products are exact there, so the result is rounded once
-        const int ia = split ? e : 2 * e, ib = split ? 4 + e : 2 * e + 1;
-        const double a = v[ia], b = v[ib], ck = cs[e], sk = sn[e];
-        v[ia] = (float)(a * ck - b * sk);
-        v[ib] = (float)(b * ck + a * sk);
+    for (int i = 0; i < HEADS; ++i) {
+      m[i] = 0;
+      if (hs + i * j.groups >= j.H) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m[i] = max(m[i], __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+      m[i] = group_max(m[i], sh);
+    }
+    static_assert(HEADS == 4, "one lane of a quad to a head");
+    const int mine = c & 3;
+    const uint32_t ml = mine & 2 ? (mine & 1 ? m[3] : m[2]) : (mine & 1 ? m[1] : m[0]);
+    const float amax = __uint_as_float(ml);
+    const float inv = ml >= TINY ? 448.0f / amax : 0.f;
+    if (sh >= 2) {
+      // a NaN or an infinity in the row makes the scale NaN, and with it the whole row
+      const int h = hs + mine * j.groups;
+      if (c < 4 && h < j.H)
+        *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
+            ml >= INF ? __uint_as_float(0x7FC00000u) : ml >= TINY ? amax / 448.0f : 1.0f;
+    }
+    const float quad[HEADS] = {
+        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0x00, 0xF, 0xF, false)),
+        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0x55, 0xF, 0xF, false)),
+        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0xAA, 0xF, 0xF, false)),
+        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0xFF, 0xF, 0xF, false))};
+#pragma unroll
+    for (int i = 0; i < HEADS; ++i) {
+      const int h = hs + i * j.groups;
+      if (h >= j.H) break;
+      float f = quad[i];
+      if (sh < 2) {   // rows of one or two lanes: no quad of their own
+        const float am = __uint_as_float(m[i]);
+        f = m[i] >= TINY ? 448.0f / am : 0.f;
+        if (c == 0)
+          *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
+              m[i] >= INF ? __uint_as_float(0x7FC00000u) : m[i] >= TINY ? am / 448.0f : 1.0f;
       }
-    }
-    uint8_t *o = j.out + slot * j.out_t + (int64_t)h * j.out_h;
-    if (j.fmt == IDX_K_FP8_E4M3) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-      m = group_max(m, sh);
-      const float amax = __uint_as_float(m);
-      const bool some = m >= TINY;
-      const float inv = some ? 448.0f / amax : 0.f;
       float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = v[e] * inv;
+      for (int e = 0; e < 8; ++e) y[e] = v[i][e] * f;
       if (live) {
+        uint8_t *o = out + (int64_t)h * j.out_h;
         const uint32_t w0 = e4m3x4(y), w1 = e4m3x4(y + 4);
         if (split) {
           *(uint32_t *)(o + e0) = w0;
@@ -197,54 +272,62 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
         } else {
           *(uint2 *)(o + e0) = make_uint2(w0, w1);
         }
-        // a NaN or an infinity in the row makes the scale NaN, and with it the whole row
-        if (c == 0)
-          *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
-              m >= INF ? __uint_as_float(0x7FC00000u) : some ? amax / 448.0f : 1.0f;
       }
-    } else if (j.fmt == IDX_K_MXFP4) {
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < HEADS; ++i) {
+    const int h = hs + i * j.groups;
+    if (h >= j.H) break;
+    uint8_t *o = out + (int64_t)h * j.out_h;
+    float *x = v[i];
+    if (j.fmt == IDX_K_MXFP4) {
       // The lane's two groups of four lie in blocks of 32 of their own when it holds the halves of
       // pairs: bring the values back into order, lane c holding elements 8c .. 8c + 7.
       if (j.freq && j.half) {
         const int lo = (j.rot0 >> 3), n = j.rot >> 3;        // rotated lanes [lo, lo + n)
         const int base = (threadIdx.x & 63) - c;
+        const bool in = c >= lo && c < lo + n;
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int q = 2 * (c - lo) + (e >> 2);             // group of four inside the part
-          const bool in = c >= lo && c < lo + n;
           const int src = in ? lo + (q < n ? q : q - n) : c;
-          const float va = __shfl(v[e & 3], base + src), vb = __shfl(v[4 + (e & 3)], base + src);
-          w[e] = in ? (q < n ? va : vb) : v[e];
+          const float va = __shfl(x[e & 3], base + src), vb = __shfl(x[4 + (e & 3)], base + src);
+          w[e] = in ? (q < n ? va : vb) : x[e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = w[e];
+        for (int e = 0; e < 8; ++e) x[e] = w[e];
       }
       uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+      for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
       m = group_max(m, 2);       // 4 lanes hold a block of 32
       const int ex = (int)(m >> 23) - 127 - 2;
       const int e8 = m >= TINY ? min(max(ex + 127, 0), 254) : 0;
-      const float inv = m >= TINY ? __uint_as_float((uint32_t)(254 - e8) << 23) : 0.f;
+      // 2^(e8 - 127) divides the values; 2^127 leaves none of a block of zeros
+      const float unit = m >= TINY ? __uint_as_float((uint32_t)e8 << 23) : 0x1p127f;
       if (live) {
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w |= e2m1(v[e] * inv) << (4 * e);
+        uint32_t w = 0;   // to nearest even, saturating
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], unit, 0);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[2], x[3], unit, 1);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[4], x[5], unit, 2);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[6], x[7], unit, 3);
         *(uint32_t *)(o + c * 4) = w;
         if ((c & 3) == 0)
           j.scale[slot * j.scale_t + (int64_t)h * j.scale_h + (c >> 2)] = m >= INF ? 0xFFu : (uint8_t)e8;
       }
     } else if (live) {
-      if (j.fmt == IDX_K_F32) {
-        *(float4 *)(o + 4 * e0) = make_float4(v[0], v[1], v[2], v[3]);
-        *(float4 *)(o + 4 * e1) = make_float4(v[4], v[5], v[6], v[7]);
+      if (F32 && j.fmt == IDX_K_F32) {
+        *(float4 *)(o + 4 * e0) = make_float4(x[0], x[1], x[2], x[3]);
+        *(float4 *)(o + 4 * e1) = make_float4(x[4], x[5], x[6], x[7]);
       } else {
         uint4 w;
         if (j.fmt == IDX_K_BF16)
-          w = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+          w = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
         else
-          w = make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+          w = make_uint4(pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7]));
         if (split) {
           *(uint2 *)(o + 2 * e0) = make_uint2(w.x, w.y);
           *(uint2 *)(o + 2 * e1) = make_uint2(w.z, w.w);
@@ -300,7 +383,7 @@ __global__ __launch_bounds__(THREADS) void read_kernel(ReadJob j) {
         v[e] = (q & 8u ? -y : y) * sc;
       }
     } else {
-      values8(load8(p, j.fmt, 8 * c, 8 * c + 4, false), j.fmt, v);
+      values8<true>(load8<true>(p, j.fmt, 8 * c, 8 * c + 4, false), j.fmt, v);
     }
   }
   uint8_t *o = j.out + (int64_t)t * j.out_t + (int64_t)h * j.out_h;
@@ -335,14 +418,21 @@ __global__ __launch_bounds__(THREADS) void slot_check_kernel(const int32_t *slot
 hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
   int64_t blocks = 0;
   int m = 0;
+  bool f32 = false;
   for (int i = 0; i < jobs.n; ++i) {
     RowJob j = jobs.job[i];
     if (j.T <= 0 || j.H <= 0 || j.rows <= 0) continue;
     j.lanes_sh = 0;
     while ((8 << j.lanes_sh) < j.D) ++j.lanes_sh;
-    j.groups = (j.H + HEADS - 1) / HEADS;
+    f32 = f32 || j.dtype == IDX_K_F32 || j.fmt == IDX_K_F32;
+    // as many heads to a lane as still leave every SIMD eight waves: few rows spread over the machine, and
+    // run one head's code only (one row of 32 heads: 3.6 us, 4.7 us with four heads to a lane)
+    int heads = HEADS;
+    while (heads > 1 && (((int64_t)j.T * ((j.H + heads - 1) / heads)) << j.lanes_sh) < 8192 * 64) heads /= 2;
+    j.groups = (j.H + heads - 1) / heads;
     jobs.job[m] = j;
     jobs.first[m++] = (int32_t)blocks;
+    static_assert(THREADS == 256, "the kernel's units of a workgroup: 256 >> lanes_sh");
     const int per = THREADS >> j.lanes_sh;
     blocks += ((int64_t)j.T * j.groups + per - 1) / per;
     if (blocks > INT32_MAX) return hipErrorInvalidValue;
@@ -350,7 +440,10 @@ hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
   jobs.n = m;
   jobs.first[m] = (int32_t)blocks;
   if (!m) return hipSuccess;
-  hipLaunchKernelGGL(write_kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, jobs);
+  if (f32)
+    hipLaunchKernelGGL(write_kernel<true>, dim3((unsigned)blocks), dim3(THREADS), 0, s, jobs);
+  else
+    hipLaunchKernelGGL(write_kernel<false>, dim3((unsigned)blocks), dim3(THREADS), 0, s, jobs);
   return hipGetLastError();
 }
 
