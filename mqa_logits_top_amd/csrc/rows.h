@@ -48,8 +48,9 @@ struct ReadJob {
   int64_t out_t, out_h;
   int32_t T, H, D;
   int32_t fmt, dtype;
+  int32_t lanes_sh;        // filled by launch_read
 };
-hipError_t launch_read(const ReadJob &j, hipStream_t s);
+hipError_t launch_read(ReadJob &j, hipStream_t s);
 
 // Debug check of slot lists: a slot inside [0, rows) named twice raises *word.
 hipError_t launch_slot_check(const int32_t *slot, int32_t T, int64_t rows, uint32_t *word, hipStream_t s);

@@ -339,29 +339,54 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
   }
 }
 
-__device__ __constant__ const float E2M1_VALUE[8] = {0.f, 0.5f, 1.f, 1.5f, 2.f, 3.f, 4.f, 6.f};
-
-// One lane to 8 elements of a row.
+// One lane to 8 elements of a row, READS rows: their loads are under way together.
+constexpr int READS = 4;
+template <int FMT>   // the cache's; IDX_K_BF16 stands for both 16-bit ones
 __global__ __launch_bounds__(THREADS) void read_kernel(ReadJob j) {
-  const int n = j.D / 8;
-  const int64_t per = (int64_t)j.H * n;
-  const int64_t x = (int64_t)blockIdx.x * THREADS + threadIdx.x;
-  if (x >= (int64_t)j.T * per) return;
-  const int t = (int)(x / per);
-  const int r = (int)(x - t * per);
-  const int h = r / n, c = r - h * n;
-  const int64_t row = j.list ? (int64_t)j.list[t] : (int64_t)t;
-  float v[8];
+  constexpr bool F32 = FMT == IDX_K_F32;
+  const int c = threadIdx.x & ((1 << j.lanes_sh) - 1);
+  const bool live = c * 8 < j.D;
+  const uint32_t units = (uint32_t)j.T * (uint32_t)j.H, per = THREADS >> j.lanes_sh;
+  const uint32_t first = blockIdx.x * per * READS + (threadIdx.x >> j.lanes_sh);
+  uint32_t t[READS], h[READS];
+  int32_t row[READS];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  if (row >= 0 && row < j.rows) {
-    const uint8_t *p = j.data + row * j.data_t + (int64_t)h * j.data_h;
-    const uint8_t *s = j.scale + row * j.scale_t + (int64_t)h * j.scale_h;
-    if (j.fmt == IDX_K_FP8_E4M3) {
+  for (int i = 0; i < READS; ++i) {
+    const uint32_t u = first + i * per;
+    t[i] = j.H == 1 ? u : u / (uint32_t)j.H;
+    h[i] = u - t[i] * (uint32_t)j.H;
+    row[i] = u < units && live ? j.list ? j.list[t[i]] : (int32_t)t[i] : -1;
+    if (row[i] >= j.rows) row[i] = -1;
+  }
+  Raw<F32> raw[READS];
+  uint32_t scale[READS];
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    if (row[i] < 0) continue;
+    const uint8_t *p = j.data + row[i] * j.data_t + (int64_t)h[i] * j.data_h;
+    if constexpr (FMT == IDX_K_FP8_E4M3) {
       const uint2 w = *(const uint2 *)(p + 8 * c);
-      const float sc = *(const float *)s;
-      const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.x, true);
-      const auto d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, false), f = __builtin_amdgcn_cvt_pk_f32_fp8((int)w.y, true);
+      raw[i].w[0] = make_uint4(w.x, w.y, 0u, 0u);
+      scale[i] = *(const uint32_t *)(j.scale + row[i] * j.scale_t + (int64_t)h[i] * j.scale_h);
+    } else if constexpr (FMT == IDX_K_MXFP4) {
+      raw[i].w[0] = make_uint4(*(const uint32_t *)(p + 4 * c), 0u, 0u, 0u);
+      scale[i] = (j.scale + row[i] * j.scale_t + (int64_t)h[i] * j.scale_h)[c >> 2];
+    } else {
+      raw[i] = load8<F32>(p, F32 ? IDX_K_F32 : IDX_K_BF16, 8 * c, 8 * c + 4, false);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < READS; ++i) {
+    if (first + i * per >= units || !live) continue;
+    float v[8];
+    if (row[i] < 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    } else if constexpr (FMT == IDX_K_FP8_E4M3) {
+      const float sc = __uint_as_float(scale[i]);
+      const int w0 = (int)raw[i].w[0].x, w1 = (int)raw[i].w[0].y;
+      const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(w0, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w0, true);
+      const auto d = __builtin_amdgcn_cvt_pk_f32_fp8(w1, false), f = __builtin_amdgcn_cvt_pk_f32_fp8(w1, true);
       v[0] = a[0] * sc;
       v[1] = a[1] * sc;
       v[2] = b[0] * sc;
@@ -370,32 +395,36 @@ __global__ __launch_bounds__(THREADS) void read_kernel(ReadJob j) {
       v[5] = d[1] * sc;
       v[6] = f[0] * sc;
       v[7] = f[1] * sc;
-    } else if (j.fmt == IDX_K_MXFP4) {
-      const uint32_t w = *(const uint32_t *)(p + 4 * c);
-      const uint32_t e8 = s[c >> 2];
+    } else if constexpr (FMT == IDX_K_MXFP4) {
+      const uint32_t w = raw[i].w[0].x, e8 = scale[i];
       // E8M0 code 0 stands for 2^-127, a subnormal; 0xFF is NaN
-      const float sc = e8 == 0xFFu ? __uint_as_float(0x7FC00000u)
-                                   : __uint_as_float(e8 ? e8 << 23 : 0x00400000u);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t q = w >> (4 * e);
-        const float y = E2M1_VALUE[q & 7u];
-        v[e] = (q & 8u ? -y : y) * sc;
-      }
+      const float sc = e8 == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(e8 ? e8 << 23 : 0x00400000u);
+      const auto a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+      const auto b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+      const auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+      const auto f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+      v[0] = a[0] * sc;
+      v[1] = a[1] * sc;
+      v[2] = b[0] * sc;
+      v[3] = b[1] * sc;
+      v[4] = d[0] * sc;
+      v[5] = d[1] * sc;
+      v[6] = f[0] * sc;
+      v[7] = f[1] * sc;
     } else {
-      values8<true>(load8<true>(p, j.fmt, 8 * c, 8 * c + 4, false), j.fmt, v);
+      values8<F32>(raw[i], j.fmt, v);
     }
-  }
-  uint8_t *o = j.out + (int64_t)t * j.out_t + (int64_t)h * j.out_h;
-  if (j.dtype == IDX_K_F32) {
-    *(float4 *)(o + 32 * c) = make_float4(v[0], v[1], v[2], v[3]);
-    *(float4 *)(o + 32 * c + 16) = make_float4(v[4], v[5], v[6], v[7]);
-  } else if (j.dtype == IDX_K_BF16) {
-    *(uint4 *)(o + 16 * c) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-  } else {
-    *(uint4 *)(o + 16 * c) =
-        make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    uint8_t *o = j.out + (int64_t)t[i] * j.out_t + (int64_t)h[i] * j.out_h;
+    if (j.dtype == IDX_K_F32) {
+      *(float4 *)(o + 32 * c) = make_float4(v[0], v[1], v[2], v[3]);
+      *(float4 *)(o + 32 * c + 16) = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (j.dtype == IDX_K_BF16) {
+      *(uint4 *)(o + 16 * c) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+      *(uint4 *)(o + 16 * c) =
+          make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
+    }
   }
 }
 
@@ -415,6 +444,13 @@ __global__ __launch_bounds__(THREADS) void slot_check_kernel(const int32_t *slot
 
 }  // namespace
 
+// log2 of the lanes of a row: the power of two at or above D / 8
+static int lanes_of(int32_t D) {
+  int sh = 0;
+  while ((8 << sh) < D) ++sh;
+  return sh;
+}
+
 hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
   int64_t blocks = 0;
   int m = 0;
@@ -422,8 +458,7 @@ hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
   for (int i = 0; i < jobs.n; ++i) {
     RowJob j = jobs.job[i];
     if (j.T <= 0 || j.H <= 0 || j.rows <= 0) continue;
-    j.lanes_sh = 0;
-    while ((8 << j.lanes_sh) < j.D) ++j.lanes_sh;
+    j.lanes_sh = lanes_of(j.D);
     f32 = f32 || j.dtype == IDX_K_F32 || j.fmt == IDX_K_F32;
     // as many heads to a lane as still leave every SIMD eight waves: few rows spread over the machine, and
     // run one head's code only (one row of 32 heads: 3.6 us, 4.7 us with four heads to a lane)
@@ -447,12 +482,20 @@ hipError_t launch_rows(RowJobs &jobs, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_read(const ReadJob &j, hipStream_t s) {
-  const int64_t total = (int64_t)j.T * j.H * (j.D / 8);
-  if (total <= 0) return hipSuccess;
-  const int64_t blocks = (total + THREADS - 1) / THREADS;
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(read_kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, j);
+hipError_t launch_read(ReadJob &j, hipStream_t s) {
+  if (j.T <= 0 || j.H <= 0) return hipSuccess;
+  j.lanes_sh = lanes_of(j.D);
+  const int64_t per = (THREADS >> j.lanes_sh) * READS;
+  const int64_t blocks = ((int64_t)j.T * j.H + per - 1) / per;
+  const dim3 grid((unsigned)blocks), threads(THREADS);
+  if (j.fmt == IDX_K_FP8_E4M3)
+    hipLaunchKernelGGL(read_kernel<IDX_K_FP8_E4M3>, grid, threads, 0, s, j);
+  else if (j.fmt == IDX_K_MXFP4)
+    hipLaunchKernelGGL(read_kernel<IDX_K_MXFP4>, grid, threads, 0, s, j);
+  else if (j.fmt == IDX_K_F32)
+    hipLaunchKernelGGL(read_kernel<IDX_K_F32>, grid, threads, 0, s, j);
+  else
+    hipLaunchKernelGGL(read_kernel<IDX_K_BF16>, grid, threads, 0, s, j);
   return hipGetLastError();
 }
 

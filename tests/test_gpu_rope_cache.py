@@ -212,6 +212,17 @@ def test_not_finite_stays_visible():
         assert got[bad].isnan().all() and torch.equal(got[~bad], want[~bad])
 
 
+def test_every_mxfp4_code():
+    """Reading back every code under every E8M0 scale: 2^-127 (a subnormal) and NaN among them."""
+    e8 = torch.arange(256, dtype=torch.uint8).view(256, 1, 1)
+    data = (torch.arange(16) | (torch.arange(16).flip(0) << 4)).to(torch.uint8).expand(256, 1, 16).contiguous()
+    c = idx.Cache(data.cuda(), e8.cuda(), D=32, fmt=FP4)
+    got = idx.idx_cache_read(c, dtype=torch.float32).cpu().double().numpy()
+    with np.errstate(over="ignore"):
+        want = read_mxfp4(data.numpy(), e8.numpy()).astype(np.float32).astype(np.float64)
+    assert np.array_equal(got, want, equal_nan=True)
+
+
 def test_smallest_values():
     """Rows and blocks below 2^-100 become zeros; the largest fp32 values survive."""
     x = torch.zeros((3, 1, 64))
