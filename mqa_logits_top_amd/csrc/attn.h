@@ -29,6 +29,8 @@ struct AttnArgs {
   float *lse;
   int32_t blocks;            // head blocks of a cache head's G query heads
   int32_t splits;            // workgroups a row's entries are divided over
+  int32_t waves;             // waves of a workgroup, over which its share is divided
+  int64_t per;               // entries of a wave
   // splits > 1: per (row, cache head, head block, split) the unnormalised out of the split's
   // heads [heads][D], then all their (maximum, sum) pairs
   float *part;
@@ -38,7 +40,8 @@ struct AttnArgs {
 struct AttnPlan {
   int32_t tiles;             // 16-head tiles a wave holds: 1 or 2
   int32_t blocks;
-  int32_t splits;
+  int32_t splits, waves;
+  int64_t per;
   size_t bytes;              // workspace
 };
 AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries);

@@ -24,6 +24,8 @@ namespace {
 constexpr int TILE = 32;      // keys of a step
 constexpr int CHUNK = 256;    // list entries resolved at a time
 constexpr int QUEUE = 512;    // rows waiting: under two tiles when a chunk is added
+constexpr int MAX_WAVES = 8;  // of a workgroup
+constexpr int MAX_SPLITS = 256;
 constexpr float NEG_INF = -__builtin_inff();
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -125,10 +127,16 @@ __device__ __forceinline__ float lse_of(float ref, float l) {
   return l == 0.f ? NEG_INF : 0.69314718055994531f * (ref + __builtin_amdgcn_logf(l));
 }
 
+// Bytes of LDS of a wave.
+constexpr int wave_lds(bool fp8, int D, bool wide) {
+  return 2 * TILE * (fp8 ? D : 2 * D) + 4 * QUEUE * (fp8 && !wide ? 2 : 1) + (fp8 ? 8 * TILE : 0);
+}
+
 // BF16: q's type; FP8: E4M3 caches (else of q's type); MT: 16-head tiles.
 // WIDE: caches past 2^32 bytes (64-bit offsets of rows instead of 32-bit ones beside a uniform base).
+// MT = 1 may run several waves a workgroup, which divide the entries and join through LDS.
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
-__global__ __launch_bounds__(64, 2) void attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(AttnArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
   constexpr int KS = D / 32;              // steps of the first product
   constexpr int DN = D / 16;              // tiles of the second product
@@ -138,14 +146,20 @@ __global__ __launch_bounds__(64, 2) void attn_kernel(AttnArgs a) {
   constexpr int NI = CH / 2;              // copies of a tile's K or V: 64 / CH rows each
   constexpr int PER = 16 / CH;            // rows a 16-lane group brings in one copy
   constexpr int NK = NI + (FP8 ? 1 : 0);  // copies of a tile's K and scales
-  __shared__ __attribute__((aligned(16))) uint8_t kbuf[TILE * RB];
-  __shared__ __attribute__((aligned(16))) uint8_t vbuf[TILE * RB];
-  __shared__ __attribute__((aligned(16))) uint32_t queue[QUEUE];
-  __shared__ __attribute__((aligned(16))) uint32_t offsets[WIDE ? 1 : QUEUE];   // the queue's rows in bytes
-  __shared__ __attribute__((aligned(16))) float scales[FP8 ? 2 * TILE : 1];
+  // a wave's LDS: K, V (the join's output afterwards), the queue, scales
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int V_AT = TILE * RB, QUEUE_AT = 2 * TILE * RB;
+  constexpr int OFFSETS_AT = QUEUE_AT + (WIDE || FP8 ? 4 * QUEUE : 0), SCALES_AT = OFFSETS_AT + (WIDE ? 0 : 4 * QUEUE);
+  constexpr int WAVE_LDS = SCALES_AT + (FP8 ? 8 * TILE : 0);
+  static_assert(WAVE_LDS == wave_lds(FP8, D, WIDE), "the launch's LDS");
+  static_assert(MT > 1 || HEADS * D * 4 <= 2 * TILE * RB, "the join's output fits K and V");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  uint8_t *const kbuf = lds + wave * WAVE_LDS, *const vbuf = kbuf + V_AT;
+  uint32_t *const queue = (uint32_t *)(kbuf + QUEUE_AT), *const offsets = (uint32_t *)(kbuf + OFFSETS_AT);
+  const float *const scales = (const float *)(kbuf + SCALES_AT);
   using Off = std::conditional_t<WIDE, uint64_t, uint32_t>;
 
-  const int lane = threadIdx.x;
+  const int lane = threadIdx.x & 63;
   const int c = lane & 15, g = lane >> 4;
   uint32_t item = blockIdx.x;
   const int split = (int)(item % (uint32_t)a.splits);
@@ -157,12 +171,12 @@ __global__ __launch_bounds__(64, 2) void attn_kernel(AttnArgs a) {
   const int head0 = kvh * a.G + hb * HEADS;                    // first query head
   const int heads = min(HEADS, a.G - hb * HEADS);
 
-  // ---- the list: this split's entries, 256 at a time, through registers into the queue of cache rows
+  // ---- the list: this wave's entries, 256 at a time, through registers into the queue of cache rows
   const int32_t win0 = a.ks ? max(a.ks[t], 0) : 0, win1 = a.ke ? min(a.ke[t], a.L) : a.L;
   const int64_t entries = (int64_t)a.n_sel << a.pool_sh;
-  const int64_t per = ((entries + a.splits - 1) / a.splits + TILE - 1) / TILE * TILE;
-  const int64_t e_end = min(entries, (split + 1) * per);
-  int64_t e_next = split * per;           // first entry whose id is not loaded
+  const int part = split * a.waves + wave;
+  const int64_t e_end = min(entries, (part + 1) * a.per);
+  int64_t e_next = part * a.per;          // first entry whose id is not loaded
   const int32_t *list = a.sel + (int64_t)t * a.ld_sel;
   // Three chunks are under way: the one that fill() appends (row), whose slots are loading (row, once it
   // is appended), and the one behind it, whose ids are loading (id).  Nothing waits for a load just issued.
@@ -465,6 +479,49 @@ __global__ __launch_bounds__(64, 2) void attn_kernel(AttnArgs a) {
 
   copies_left<0>();   // none may write LDS that is another wave's by then
 
+  if constexpr (MT == 1) {
+    if (a.waves > 1) {
+      // each wave's output, sum and reference through LDS; quads of dims exchanged against bank conflicts
+      constexpr int QUADS = D / 4;
+      float *const ml = (float *)(lds + a.waves * WAVE_LDS);    // [waves][2][16]
+      const float l = head_sum(sum[0]);
+#pragma unroll
+      for (int d = 0; d < DN; ++d)
+        *(f32x4 *)(kbuf + c * D * 4 + ((4 * d + g) ^ (c & 7)) * 16) = o[0][d];
+      if (g == 0) {
+        ml[wave * 32 + c] = ref[0];
+        ml[wave * 32 + 16 + c] = l;
+      }
+      __syncthreads();
+      for (int x = threadIdx.x; x < heads * QUADS; x += 64 * a.waves) {
+        const int h = x / QUADS, y = x % QUADS;
+        float top = NEG_INF;
+        for (int w = 0; w < a.waves; ++w) top = __builtin_fmaxf(top, ml[w * 32 + h]);
+        const float base = top == NEG_INF ? 0.f : top;
+        float total = 0.f;
+        f32x4 r = {0.f, 0.f, 0.f, 0.f};
+        for (int w = 0; w < a.waves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(ml[w * 32 + h] - base);
+          total += f * ml[w * 32 + 16 + h];
+          r += f * *(const f32x4 *)(lds + w * WAVE_LDS + h * D * 4 + (y ^ (h & 7)) * 16);
+        }
+        if (a.splits > 1) {
+          const int64_t at = (int64_t)blockIdx.x * HEADS + h;
+          *(f32x4 *)(a.part + at * D + 4 * y) = r;
+          if (y == 0) {
+            a.part_ml[2 * at] = top;
+            a.part_ml[2 * at + 1] = total;
+          }
+        } else {
+          r *= finish(total);
+          *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)(head0 + h) * a.out_h + 8 * y) =
+              make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
+          if (y == 0 && a.lse) a.lse[(int64_t)t * a.Hq + head0 + h] = lse_of(top, total);
+        }
+      }
+      return;
+    }
+  }
   // lane l holds head l % 16 and dims 16 d + 4 g + j
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -497,52 +554,72 @@ template <bool BF16, int D>
 __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEADS) {
   constexpr int QUADS = D / 4, GROUPS = MERGE / QUADS;
   __shared__ __attribute__((aligned(16))) float acc[GROUPS][D];
-  __shared__ float sums[GROUPS];
-  const int64_t th = blockIdx.x;
-  const int t = (int)(th / a.Hq), hq = (int)(th % a.Hq);
+  __shared__ float factor[MAX_SPLITS];
+  __shared__ float shared[2];
+  const uint32_t th = blockIdx.x;
+  const int t = (int)(th / (uint32_t)a.Hq), hq = (int)(th % (uint32_t)a.Hq);
   const int kvh = hq / a.G, in = hq % a.G;
   const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS;
   const int64_t at0 = ((((int64_t)t * a.Hkv + kvh) * a.blocks + in / HEADS) * a.splits) * HEADS + in % HEADS;
-  float top = NEG_INF;
-  for (int s = 0; s < a.splits; ++s) top = __builtin_fmaxf(top, a.part_ml[2 * (at0 + (int64_t)s * HEADS)]);
-  const float ref = top == NEG_INF ? 0.f : top;
-  float l = 0.f;
+  if (threadIdx.x < 64) {   // one wave: every split's reference and sum at once
+    float m[MAX_SPLITS / 64], l[MAX_SPLITS / 64];
+#pragma unroll
+    for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+      const int s = threadIdx.x + 64 * i;
+      m[i] = NEG_INF;
+      l[i] = 0.f;
+      if (s < a.splits) {
+        const float2 ml = *(const float2 *)(a.part_ml + 2 * (at0 + (int64_t)s * HEADS));
+        m[i] = ml.x;
+        l[i] = ml.y;
+      }
+    }
+    float top = m[0];
+#pragma unroll
+    for (int i = 1; i < MAX_SPLITS / 64; ++i) top = __builtin_fmaxf(top, m[i]);
+    top = wave_reduce_f32(top, [](float x, float y) { return __builtin_fmaxf(x, y); });
+    const float ref = top == NEG_INF ? 0.f : top;
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+      const int s = threadIdx.x + 64 * i;
+      const float f = __builtin_amdgcn_exp2f(m[i] - ref);
+      if (s < a.splits) {
+        factor[s] = f;
+        total += f * l[i];
+      }
+    }
+    total = wave_reduce_f32(total, [](float x, float y) { return x + y; });
+    if (threadIdx.x == 0) {
+      shared[0] = top;
+      shared[1] = total;
+    }
+  }
+  __syncthreads();
   f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-  for (int s = gr; s < a.splits; s += GROUPS) {
-    const int64_t at = at0 + (int64_t)s * HEADS;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
-    l += f * a.part_ml[2 * at + 1];
-    r += f * *(const f32x4 *)(a.part + at * D + d);
-  }
+  for (int s = gr; s < a.splits; s += GROUPS) r += factor[s] * *(const f32x4 *)(a.part + (at0 + (int64_t)s * HEADS) * D + d);
   *(f32x4 *)&acc[gr][d] = r;
-  if (d == 0) sums[gr] = l;
   __syncthreads();
   if (gr) return;
 #pragma unroll
-  for (int x = 1; x < GROUPS; ++x) {
-    r += *(const f32x4 *)&acc[x][d];
-    l += sums[x];
-  }
-  if (d) {
-    l = 0.f;
-#pragma unroll
-    for (int x = 0; x < GROUPS; ++x) l += sums[x];
-  }
-  r *= finish(l);
+  for (int x = 1; x < GROUPS; ++x) r += *(const f32x4 *)&acc[x][d];
+  r *= finish(shared[1]);
   *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)hq * a.out_h + 2 * d) =
       make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
-  if (d == 0 && a.lse) a.lse[th] = lse_of(top, l);
+  if (d == 0 && a.lse) a.lse[th] = lse_of(shared[0], shared[1]);
 }
 
+template <bool BF16, bool FP8, int D, int MT, bool WIDE>
+hipError_t launch_width(const AttnArgs &a, unsigned blocks, hipStream_t s) {
+  const size_t lds = (size_t)a.waves * wave_lds(FP8, D, WIDE) + (a.waves > 1 ? 128 * a.waves : 0);
+  hipLaunchKernelGGL((attn_kernel<BF16, FP8, D, MT, WIDE>), dim3(blocks), dim3(64 * a.waves), lds, s, a);
+  return hipGetLastError();
+}
 template <bool BF16, bool FP8, int D, int MT>
 hipError_t launch_one(const AttnArgs &a, unsigned blocks, hipStream_t s) {
-  if ((uint64_t)a.rows * a.row_bytes > 0xFFFFFFFFull) {
-    hipLaunchKernelGGL((attn_kernel<BF16, FP8, D, MT, true>), dim3(blocks), dim3(64), 0, s, a);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL((attn_kernel<BF16, FP8, D, MT, false>), dim3(blocks), dim3(64), 0, s, a);
-  return hipGetLastError();
+  return (uint64_t)a.rows * a.row_bytes > 0xFFFFFFFFull ? launch_width<BF16, FP8, D, MT, true>(a, blocks, s)
+                                                        : launch_width<BF16, FP8, D, MT, false>(a, blocks, s);
 }
 template <bool BF16, bool FP8, int D>
 hipError_t launch_tiles(const AttnArgs &a, int tiles, unsigned blocks, hipStream_t s) {
@@ -557,19 +634,35 @@ hipError_t launch_dim(const AttnArgs &a, int D, int tiles, unsigned blocks, hipS
 
 AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries) {
   AttnPlan p{};
-  p.tiles = G <= 16 ? 1 : 2;
-  int64_t items = 0;
-  for (;; p.tiles /= 2) {
-    const int32_t heads = 16 * p.tiles;
-    p.blocks = (G + heads - 1) / heads;
-    items = (int64_t)T * Hkv * p.blocks;
-    if (p.tiles == 1 || items >= 64) break;
+  const int64_t tiles = entries > 0 ? (entries + TILE - 1) / TILE : 1;
+  // 32 heads to a wave where rows alone fill the machine (2 waves a SIMD): each key is fetched once for them
+  p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 1024 ? 2 : 1;
+  const int32_t heads = 16 * p.tiles;
+  p.blocks = (G + heads - 1) / heads;
+  const int64_t items = (int64_t)T * Hkv * p.blocks;
+  // Fewer rows than that: a row's entries are divided over the waves of a workgroup, which join through LDS, or
+  // over workgroups, which a second kernel joins (4 us).  A 32-key step takes a lone wave about 1 us.
+  p.waves = p.splits = 1;
+  if (p.tiles == 1 && items <= 256) {
+    if (tiles > 32 && items < 128) {
+      // few rows, long lists: about one step to a wave.  1 row, 64 heads, 2048 keys: 9.9 us, 15.8 with eight
+      // waves alone; 8 rows: 11.8 and 17.8
+      p.waves = 4;
+      while (items * p.waves * p.splits < 1024 && p.waves * p.splits < tiles && p.splits < MAX_SPLITS) p.splits *= 2;
+    } else {
+      // 32 rows, 64 heads, 2048 keys: 17.3 us, 21.2 with four waves and two workgroups; 256 rows, 16 heads, 512
+      // keys: 15.9 us, 17.3 with one wave
+      while (p.waves < MAX_WAVES && p.waves < tiles && items * p.waves < 1024) p.waves *= 2;
+    }
+  } else if (p.tiles == 1) {
+    // whole workgroups no longer spread evenly over 256 CUs (40 rows x 8 cache heads, 2048 keys: 50 us, 66 with
+    // four waves to a workgroup), and a short list is not worth the join (64 rows x 8 cache heads, 512 keys: 30 us,
+    // 35 in two)
+    while (items * p.splits < 1024 && p.splits * 16 < tiles) p.splits *= 2;
   }
-  const int64_t most = (entries + TILE - 1) / TILE;
-  int64_t splits = items > 0 ? 2048 / items : 1;
-  splits = splits < most ? splits : most;
-  p.splits = (int32_t)(splits < 1 ? 1 : splits);
-  p.bytes = p.splits > 1 ? (size_t)items * p.splits * 16 * p.tiles * (D + 2) * 4 : 0;
+  const int64_t parts = (int64_t)p.waves * p.splits;
+  p.per = ((tiles + parts - 1) / parts) * TILE;
+  p.bytes = p.splits > 1 ? (size_t)items * p.splits * heads * (D + 2) * 4 : 0;
   return p;
 }
 
@@ -591,6 +684,8 @@ hipError_t launch_attn(AttnArgs &a, int32_t dtype, int32_t fmt, int32_t D, const
   const int heads = 16 * plan.tiles;
   a.blocks = plan.blocks;
   a.splits = plan.splits;
+  a.waves = plan.waves;
+  a.per = plan.per;
   a.part = (float *)ws;
   a.part_ml = a.part + (size_t)blocks * heads * D;
   // a negative factor turns q over instead, so that the largest product comes from the largest dot

@@ -89,8 +89,8 @@ def test_read_refusals(lib):
 
 
 def _attn(**kw):
-    base = dict(q=_rows(T=2, H=16), out=_rows(T=2, H=16, data=2 * F), k=_cache(), v=_cache(), sel=F, ld_sel=640,
-                n_sel=640, pool=1, ks=None, ke=None, slot_of_key=None, L=100, scale=0.1, lse=None)
+    base = dict(q=_rows(T=2, H=16), out=_rows(T=2, H=16, data=2 * F), k=_cache(), v=_cache(), sel=F, ld_sel=64000,
+                n_sel=64000, pool=1, ks=None, ke=None, slot_of_key=None, L=100, scale=0.1, lse=None)
     return idx.idx_attn(**(base | kw))
 
 
@@ -104,7 +104,7 @@ def test_attn_refusals(lib):
             (SHAPE, dict(q=r(T=3))), (SHAPE, dict(out=r(H=8))), (SHAPE, dict(k=_cache(H=4))),
             (SHAPE, dict(k=_cache(H=5), v=_cache(H=5))), (SHAPE, dict(v=_cache(rows=99))),
             (SHAPE, dict(k=_cache(D=64))), (SHAPE, dict(k=_cache(ld=2048))), (SHAPE, dict(v=_cache(ld_scale=16))),
-            (UNSUPPORTED, dict(k=_cache(ld=2 ** 31), v=_cache(ld=2 ** 31))), (SHAPE, dict(n_sel=-1)), (SHAPE, dict(ld_sel=639)), (SHAPE, dict(L=101)),
+            (UNSUPPORTED, dict(k=_cache(ld=2 ** 31), v=_cache(ld=2 ** 31))), (SHAPE, dict(n_sel=-1)), (SHAPE, dict(ld_sel=63999)), (SHAPE, dict(L=101)),
             (SHAPE, dict(L=-1)), (FORMAT, dict(q=r(dtype=F32), out=r(dtype=F32))), (FORMAT, dict(out=r(dtype=F16))),
             (FORMAT, dict(k=_cache(fmt=BF16))), (UNSUPPORTED, dict(k=_cache(fmt=F16), v=_cache(fmt=F16))),
             (UNSUPPORTED, dict(k=_cache(fmt=FP4), v=_cache(fmt=FP4))),
