@@ -495,45 +495,44 @@ _STORED = {IDX_K_FP8_E4M3: torch.uint8, IDX_K_MXFP4: torch.uint8, IDX_K_BF16: to
            IDX_K_F16: torch.float16, IDX_K_F32: torch.float32}
 
 
-def _want(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _on(t: torch.Tensor, device, dtype, what: str) -> int:
     """The tensor's address, if it is one the kernels can read as it stands."""
-    if t.device != device or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous {dtype} tensor on {device}, got {t.dtype} on {t.device}"
                          f"{'' if t.is_contiguous() else ', not contiguous'}")
     return t.data_ptr()
 
 
 def _rows(x: torch.Tensor, what: str) -> idx_rows:
-    if not x.is_cuda or x.dim() != 3 or x.dtype not in _VALUE or (x.shape[2] > 1 and x.stride(2) != 1):
+    dtype = _VALUE.get(x.dtype)
+    if dtype is None or not x.is_cuda or x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
         raise ValueError(f"{what}: [T, H, D] bfloat16, float16 or float32 on the GPU with a contiguous last "
                          f"dimension, got {list(x.shape)} {x.dtype} on {x.device}, strides {x.stride()}")
     T, H, D = x.shape
-    return idx_rows(x.data_ptr(), x.stride(0), x.stride(1), _VALUE[x.dtype], T, H, D)
+    ld_t, ld_h, _ = x.stride()
+    return idx_rows(x.data_ptr(), ld_t, ld_h, dtype, T, H, D)
 
 
-class _Stream:
-    """The call's stream: the one given, or the current one of the tensors' device.  Outputs and
-    workspaces allocated inside belong to it."""
+class _on_stream:
+    """The calls below run on the stream given, or on the current stream of the tensors' device: outputs and
+    workspaces allocated inside belong to it.  Where that is the current stream already, there is nothing to
+    set (guard is None) and only its handle is looked up."""
+
+    __slots__ = ("guard", "handle")
 
     def __init__(self, device: torch.device, stream):
-        self.guard = None
-        if stream is not None:
-            _want(stream.device == device, f"a stream of {stream.device} for tensors on {device}")
-            self.guard = torch.cuda.stream(stream)
-        elif device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.device, self.stream = device, stream
+        if stream is None:
+            self.guard = None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+            self.handle = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if stream.device != device:
+                raise ValueError(f"a stream of {stream.device} for tensors on {device}")
+            self.guard, self.handle = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        stream = self.stream if self.stream is not None else torch.cuda.current_stream(self.device)
-        return ctypes.c_void_p(stream.cuda_stream)
+        return self.handle
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -553,9 +552,10 @@ class Rotary:
     """Rotary positions of dims [rot0, rot0 + 2 len(freq)) of a head; keep one and pass it to every call."""
 
     def __init__(self, freq: torch.Tensor, rot0: int = 0, layout: int = IDX_ROPE_HALF, mscale: float = 1.0):
-        _want(freq.is_cuda and freq.dim() == 1, f"freq: one dimension, on the GPU, got {list(freq.shape)} on "
-              f"{freq.device}")
+        if not freq.is_cuda or freq.dim() != 1:
+            raise ValueError(f"freq: one dimension, on the GPU, got {list(freq.shape)} on {freq.device}")
         self.freq, self.rot0, self.layout, self.mscale = freq, rot0, layout, mscale
+        self.device = freq.device
         self._args = (_on(freq, freq.device, torch.float64, "freq"), 2 * int(freq.numel()), rot0, layout, mscale)
 
     @staticmethod
@@ -566,9 +566,11 @@ class Rotary:
 
     def struct(self, pos: torch.Tensor, x: torch.Tensor, inverse: bool = False) -> idx_rotary:
         freq, rot, rot0, layout, mscale = self._args
-        _want(pos is not None and pos.shape == x.shape[:1], "pos: [T], one position a row")
-        _want(self.freq.device == x.device, f"a Rotary on {self.freq.device} for rows on {x.device}")
-        return idx_rotary(freq, _on(pos, x.device, torch.int32, "pos"), rot, rot0, layout, int(inverse), mscale)
+        if pos is None or pos.shape != x.shape[:1]:
+            raise ValueError("pos: [T], one position a row")
+        if self.device != x.device:
+            raise ValueError(f"a Rotary on {self.device} for rows on {x.device}")
+        return idx_rotary(freq, _on(pos, self.device, torch.int32, "pos"), rot, rot0, layout, inverse, mscale)
 
 
 class Cache:
@@ -579,34 +581,40 @@ class Cache:
 
     def __init__(self, data: torch.Tensor, scale: Optional[torch.Tensor] = None, D: Optional[int] = None,
                  fmt: int = IDX_K_FP8_E4M3):
-        _want(fmt in _STORED, f"unknown cache format {fmt}")
-        _want(data.is_cuda and data.dim() == 3 and data.dtype == _STORED[fmt],
-              f"cache data: [slots, H, D] {_STORED[fmt]} on the GPU, got {list(data.shape)} {data.dtype} on "
-              f"{data.device}")
+        if fmt not in _STORED:
+            raise ValueError(f"unknown cache format {fmt}")
+        if not data.is_cuda or data.dim() != 3 or data.dtype != _STORED[fmt]:
+            raise ValueError(f"cache data: [slots, H, D] {_STORED[fmt]} on the GPU, got {list(data.shape)} "
+                             f"{data.dtype} on {data.device}")
         rows, H, width = data.shape
         D = width * (2 if fmt == IDX_K_MXFP4 else 1) if D is None else D
-        _want(width == (D // 2 if fmt == IDX_K_MXFP4 else D), f"cache data: {width} wide for D = {D}")
-        _want(width <= 1 or data.stride(2) == 1, "cache data: a contiguous last dimension")
-        _want(H <= 1 or data.stride(1) == width, "cache data: a slot's heads follow each other")
+        if width != (D // 2 if fmt == IDX_K_MXFP4 else D):
+            raise ValueError(f"cache data: {width} wide for D = {D}")
+        if (width > 1 and data.stride(2) != 1) or (H > 1 and data.stride(1) != width):
+            raise ValueError(f"cache data: a slot's heads, and a head's values, follow each other; strides "
+                             f"{data.stride()}")
         ld_scale, shape = 0, {IDX_K_FP8_E4M3: (rows, H), IDX_K_MXFP4: (rows, H, D // 32)}.get(fmt)
-        if shape is not None:
-            want = torch.float32 if fmt == IDX_K_FP8_E4M3 else torch.uint8
-            _want(scale is not None and scale.device == data.device and scale.dtype == want
-                  and tuple(scale.shape) == shape, f"cache scale: {list(shape)} {want} on {data.device}")
-            inner = scale[:1]
-            _want(rows == 0 or inner.is_contiguous(), "cache scale: a slot's scales follow each other")
-            ld_scale = scale.stride(0)
+        if shape is None:
+            if scale is not None:
+                raise ValueError("a 16- or 32-bit cache has no scale")
         else:
-            _want(scale is None, "a 16- or 32-bit cache has no scale")
+            want = torch.float32 if fmt == IDX_K_FP8_E4M3 else torch.uint8
+            if scale is None or scale.device != data.device or scale.dtype != want or tuple(scale.shape) != shape:
+                raise ValueError(f"cache scale: {list(shape)} {want} on {data.device}")
+            if rows and not scale[:1].is_contiguous():
+                raise ValueError(f"cache scale: a slot's scales follow each other; strides {scale.stride()}")
+            ld_scale = scale.stride(0)
         self.data, self.scale, self.fmt, self.D = data, scale, fmt, D
-        self.device = data.device
+        self.rows, self.H, self.device = rows, H, data.device
         ld = data.stride(0) * (2 if fmt == IDX_K_MXFP4 else 1)
-        self._args = (data.data_ptr(), None if scale is None else scale.data_ptr(), rows, ld, ld_scale, fmt, H, D)
+        self._struct = idx_cache(data.data_ptr(), None if scale is None else scale.data_ptr(), rows, ld, ld_scale,
+                                 fmt, H, D)
 
     @staticmethod
     def empty(rows: int, H: int, D: int, fmt: int = IDX_K_FP8_E4M3, device="cuda") -> "Cache":
         """A cache of zeros."""
-        _want(fmt in _STORED, f"unknown cache format {fmt}")
+        if fmt not in _STORED:
+            raise ValueError(f"unknown cache format {fmt}")
         data = torch.zeros((rows, H, D // 2 if fmt == IDX_K_MXFP4 else D), dtype=_STORED[fmt], device=device)
         scale = None
         if fmt == IDX_K_FP8_E4M3:
@@ -615,16 +623,8 @@ class Cache:
             scale = torch.zeros((rows, H, D // 32), dtype=torch.uint8, device=device)
         return Cache(data, scale, D=D, fmt=fmt)
 
-    @property
-    def rows(self) -> int:
-        return int(self.data.shape[0])
-
-    @property
-    def H(self) -> int:
-        return int(self.data.shape[1])
-
     def struct(self) -> idx_cache:
-        return idx_cache(*self._args)
+        return self._struct
 
 
 @dataclass
@@ -642,54 +642,61 @@ def idx_rope(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, out: Optional[t
              inverse: bool = False, stream=None) -> torch.Tensor:
     """x [T, H, D] rotated to positions pos [T]; out may be x."""
     rows, r = _rows(x, "x"), rotary.struct(pos, x, inverse)
-    with _Stream(x.device, stream) as st:
+    device = rotary.device
+    with _on_stream(device, stream) as st:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        else:
-            _want(out.device == x.device, f"out on {out.device} for x on {x.device}")
-        to = _rows(out, "out")
-        _check("idx_rope", load_library().idx_rope(rows, r, to, st))
+            out = x.new_empty(x.shape)
+        elif out.device != device:
+            raise ValueError(f"out on {out.device} for x on {device}")
+        s = load_library().idx_rope(rows, r, _rows(out, "out"), st)
+    if s:
+        raise IdxError("idx_rope", s)
     return out
 
 
 def idx_cache_write(writes, stream=None) -> None:
     """Rotate (where asked), quantise and store every Write's rows, in one launch."""
     n = len(writes)
-    _want(n <= IDX_MAX_WRITES, f"{n} writes in a call, at most {IDX_MAX_WRITES}")
+    if n > IDX_MAX_WRITES:
+        raise ValueError(f"{n} writes in a call, at most {IDX_MAX_WRITES}")
     if n == 0:
         return
-    device = writes[0].x.device
+    device = writes[0].cache.device
     args, keep = (idx_write * n)(), []
     for a, w in zip(args, writes):
-        a.x = _rows(w.x, "x")
-        _want(w.x.device == device and w.cache.device == device, "every row array and cache of a call on one device")
+        x, cache = w.x, w.cache
+        a.x, a.to = _rows(x, "x"), cache._struct
+        if x.device != device or cache.device != device:
+            raise ValueError("every row array and cache of a call on one device")
         if w.rotary is not None:
-            keep.append(w.rotary.struct(w.pos, w.x, w.inverse))
+            keep.append(w.rotary.struct(w.pos, x, w.inverse))
             a.rotary = ctypes.pointer(keep[-1])
         if w.slot is not None:
-            _want(w.slot.shape == w.x.shape[:1], "slot: [T], one slot a row")
+            if w.slot.shape != x.shape[:1]:
+                raise ValueError("slot: [T], one slot a row")
             a.slot = _on(w.slot, device, torch.int32, "slot")
-        a.to = w.cache.struct()
-    with _Stream(device, stream) as st:
-        _check("idx_cache_write", load_library().idx_cache_write(args, n, st))
+    with _on_stream(device, stream) as st:
+        s = load_library().idx_cache_write(args, n, st)
+    if s:
+        raise IdxError("idx_cache_write", s)
 
 
 def idx_cache_read(cache: Cache, rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                    dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """Values [N, H, D] of the slots rows [N] (None: every slot in order); zeros for a slot outside the cache."""
-    device = cache.device
-    at = None
+    device, at, n = cache.device, None, cache.rows
     if rows is not None:
-        _want(rows.dim() == 1, "rows: one dimension")
-        at = _on(rows, device, torch.int32, "rows")
-    n = cache.rows if rows is None else int(rows.shape[0])
-    with _Stream(device, stream) as st:
+        if rows.dim() != 1:
+            raise ValueError("rows: one dimension")
+        at, n = _on(rows, device, torch.int32, "rows"), rows.shape[0]
+    with _on_stream(device, stream) as st:
         if out is None:
-            out = torch.empty((n, cache.H, cache.D), dtype=dtype, device=device)
-        else:
-            _want(out.device == device and out.shape[0] == n, f"out: {n} rows on {device}")
-        to = _rows(out, "out")
-        _check("idx_cache_read", load_library().idx_cache_read(cache.struct(), at, to, st))
+            out = cache.data.new_empty((n, cache.H, cache.D), dtype=dtype)
+        elif out.device != device or out.shape[0] != n:
+            raise ValueError(f"out: {n} rows on {device}")
+        s = load_library().idx_cache_read(cache._struct, at, _rows(out, "out"), st)
+    if s:
+        raise IdxError("idx_cache_read", s)
     return out
 
 
@@ -699,42 +706,51 @@ def idx_sparse_attn(q: torch.Tensor, k: Cache, v: Cache, sel: torch.Tensor, scal
                     lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, with_lse: bool = True,
                     stream=None):
     """Attention of q [T, Hq, D] over the keys (pool 1) or blocks of keys that sel [T, n] lists; (out, lse)."""
-    device = q.device
-    T, Hq, _ = q.shape if q.dim() == 3 else (0, 0, 0)
-    a = idx_attn(q=_rows(q, "q"), k=k.struct(), v=v.struct(), pool=pool, scale=scale)
-    _want(k.device == device and v.device == device, f"caches on {k.device} and {v.device} for q on {device}")
-    if (sel.device != device or sel.dtype != torch.int32 or sel.dim() != 2 or sel.shape[0] != T
-            or (sel.shape[1] > 1 and sel.stride(1) != 1)):
+    device, rows = k.device, _rows(q, "q")
+    T, Hq = rows.T, rows.H
+    if q.device != device or v.device != device:
+        raise ValueError(f"caches on {k.device} and {v.device} for q on {q.device}")
+    if (sel.dtype is not torch.int32 or sel.device != device or sel.dim() != 2 or sel.shape[0] != T
+            or (sel.stride(1) != 1 and sel.shape[1] > 1)):
         raise ValueError(f"sel: [T, n] int32 on {device} with a contiguous last dimension, got {list(sel.shape)} "
                          f"{sel.dtype} on {sel.device}")
-    a.sel, a.ld_sel, a.n_sel = sel.data_ptr(), sel.stride(0), sel.shape[1]
+    a_ks = a_ke = table = None
+    L = k.rows
     if ks is not None or ke is not None:
-        _want(ks is not None and ke is not None and ks.shape == (T,) and ke.shape == (T,), "ks and ke: [T] both")
-        a.ks, a.ke = _on(ks, device, torch.int32, "ks"), _on(ke, device, torch.int32, "ke")
-    if slot_of_key is None:
-        a.L = k.rows
-    else:
-        _want(slot_of_key.dim() == 1, "slot_of_key: one dimension")
-        a.L, a.slot_of_key = slot_of_key.shape[0], _on(slot_of_key, device, torch.int32, "slot_of_key")
+        if ks is None or ke is None or ks.shape != (T,) or ke.shape != (T,):
+            raise ValueError("ks and ke: [T] both")
+        a_ks, a_ke = _on(ks, device, torch.int32, "ks"), _on(ke, device, torch.int32, "ke")
+    if slot_of_key is not None:
+        if slot_of_key.dim() != 1:
+            raise ValueError("slot_of_key: one dimension")
+        L, table = slot_of_key.shape[0], _on(slot_of_key, device, torch.int32, "slot_of_key")
     lib = load_library()
-    with _Stream(device, stream) as st:
+    with _on_stream(device, stream) as st:
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        else:
-            _want(out.device == device, f"out on {out.device} for q on {device}")
+            out = q.new_empty(q.shape)
+        elif out.device != device:
+            raise ValueError(f"out on {out.device} for q on {device}")
         if lse is None:
             if with_lse:
-                lse = torch.empty((T, Hq), dtype=torch.float32, device=device)
-        else:
-            _want(lse.shape == (T, Hq), f"lse: {[T, Hq]}")
-        a.out = _rows(out, "out")
-        if lse is not None:
-            a.lse = _on(lse, device, torch.float32, "lse")
-        need = ctypes.c_size_t()
-        _check("idx_sparse_attn_workspace", lib.idx_sparse_attn_workspace(a, need))
+                lse = q.new_empty((T, Hq), dtype=torch.float32)
+        elif lse.shape != (T, Hq):
+            raise ValueError(f"lse: {[T, Hq]}")
+        a = idx_attn(rows, _rows(out, "out"), k._struct, v._struct, sel.data_ptr(), sel.stride(0), sel.shape[1], pool,
+                     a_ks, a_ke, table, L, scale, None if lse is None else _on(lse, device, torch.float32, "lse"))
+        at, size = None, 0
         if ws is None:
-            ws = _workspace(need.value, device)
+            need = ctypes.c_size_t()
+            s = lib.idx_sparse_attn_workspace(a, need)
+            if s:
+                raise IdxError("idx_sparse_attn_workspace", s)
+            size = need.value
+            if size:
+                ws = torch.empty(size, dtype=torch.uint8, device=device)
         else:
-            _on(ws, device, torch.uint8, "ws")
-        _check("idx_sparse_attn", lib.idx_sparse_attn(a, _ptr(ws), 0 if ws is None else ws.numel(), st))
+            size = ws.numel()
+        if ws is not None:
+            at = _on(ws, device, torch.uint8, "ws")
+        s = lib.idx_sparse_attn(a, at, size, st)
+    if s:
+        raise IdxError("idx_sparse_attn", s)
     return out, lse
