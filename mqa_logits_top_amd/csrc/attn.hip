@@ -146,13 +146,14 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
   constexpr int NI = CH / 2;              // copies of a tile's K or V: 64 / CH rows each
   constexpr int PER = 16 / CH;            // rows a 16-lane group brings in one copy
   constexpr int NK = NI + (FP8 ? 1 : 0);  // copies of a tile's K and scales
+  constexpr int OUT_CH = D / 8;           // 16-byte chunks of a row of out
   // a wave's LDS: K, V (the join's output afterwards), the queue, scales
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int V_AT = TILE * RB, QUEUE_AT = 2 * TILE * RB;
   constexpr int OFFSETS_AT = QUEUE_AT + (WIDE || FP8 ? 4 * QUEUE : 0), SCALES_AT = OFFSETS_AT + (WIDE ? 0 : 4 * QUEUE);
   constexpr int WAVE_LDS = SCALES_AT + (FP8 ? 8 * TILE : 0);
   static_assert(WAVE_LDS == wave_lds(FP8, D, WIDE), "the launch's LDS");
-  static_assert(MT > 1 || HEADS * D * 4 <= 2 * TILE * RB, "the join's output fits K and V");
+  static_assert(HEADS * D * (MT > 1 ? 2 : 4) <= 2 * TILE * RB, "the output fits K and V");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   uint8_t *const kbuf = lds + wave * WAVE_LDS, *const vbuf = kbuf + V_AT;
   uint32_t *const queue = (uint32_t *)(kbuf + QUEUE_AT), *const offsets = (uint32_t *)(kbuf + OFFSETS_AT);
@@ -527,8 +528,8 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
   for (int m = 0; m < MT; ++m) {
     const float l = head_sum(sum[m]);
     const int h = m * 16 + c;
-    if (h >= heads) continue;
     if (a.splits > 1) {
+      if (h >= heads) continue;
       const int64_t at = (int64_t)blockIdx.x * HEADS + h;
       if (g == 0) {
         a.part_ml[2 * at] = ref[m];
@@ -538,13 +539,23 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
       for (int d = 0; d < DN; ++d) *(f32x4 *)(a.part + at * D + 16 * d + 4 * g) = o[m][d];
     } else {
       const float f = finish(l);
-      uint8_t *dst = a.out + (int64_t)t * a.out_t + (int64_t)(head0 + h) * a.out_h;
 #pragma unroll
       for (int d = 0; d < DN; ++d)
-        *(uint2 *)(dst + 2 * (16 * d + 4 * g)) =
+        *(uint2 *)(kbuf + h * 2 * D + (((2 * d + (g >> 1)) ^ (h & (OUT_CH - 1))) << 4) + 8 * (g & 1)) =
             make_uint2(pack2<BF16>(o[m][d][0] * f, o[m][d][1] * f), pack2<BF16>(o[m][d][2] * f, o[m][d][3] * f));
-      if (g == 0 && a.lse) a.lse[(int64_t)t * a.Hq + head0 + h] = lse_of(ref[m], l);
+      if (g == 0 && h < heads && a.lse) a.lse[(int64_t)t * a.Hq + head0 + h] = lse_of(ref[m], l);
     }
+  }
+  if (a.splits > 1) return;
+  // through LDS, so that whole rows are stored at a time
+  wave_sync();
+  uint8_t *const dst = a.out + (int64_t)t * a.out_t;
+#pragma unroll
+  for (int i = 0; i < HEADS * OUT_CH / 64; ++i) {
+    const int h = i * (64 / OUT_CH) + lane / OUT_CH, ch = lane & (OUT_CH - 1);
+    if (h < heads)
+      *(u32x4 *)(dst + (int64_t)(head0 + h) * a.out_h + 16 * ch) =
+          *(const u32x4 *)(kbuf + h * 2 * D + ((ch ^ (h & (OUT_CH - 1))) << 4));
   }
 }
 
