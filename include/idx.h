@@ -373,7 +373,8 @@ idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double fact
                           double beta_fast, double beta_slow, double *freq, double *mscale);
 
 /* Rows of x rotated into out (same sizes and type).  out may be x itself, with the same
- * strides; otherwise the two share no byte.  D a multiple of 8, at most 512. */
+ * strides; otherwise the two share no byte.  D a multiple of 8, at most 512; T * H below 2^31 over the
+ * power of two at or above D / 8 (that holds for every entry point with idx_rows but idx_sparse_attn). */
 idx_status idx_rope(const idx_rows *x, const idx_rotary *r, const idx_rows *out, void *stream);
 
 /* A cache of `rows` slots with H rows of D values each; slot s, head h at s * ld + h * D elements.
@@ -430,7 +431,7 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
  * entries has no influence beyond the rounding of sums; results are bitwise repeatable.
  * q and out share type and sizes, IDX_K_BF16 or IDX_K_F16; the caches are of that type or E4M3, both
  * alike, with the same slots and strides; D = 64 or 128.  Products run on the matrix cores with fp32 accumulation, E4M3 codes
- * converted exactly; weights are rounded to 16 bits before the second product (2^-9 relative in
+ * converted exactly; T * Hq below 2^26; weights are rounded to 16 bits before the second product (2^-9 relative in
  * bf16, 2^-12 in fp16: bf16 wherever v is E4M3), sums and maxima are fp32.
  * ws: idx_sparse_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap
  * in time need one each. */

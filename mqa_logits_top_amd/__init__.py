@@ -554,9 +554,13 @@ class Rotary:
     def __init__(self, freq: torch.Tensor, rot0: int = 0, layout: int = IDX_ROPE_HALF, mscale: float = 1.0):
         if not freq.is_cuda or freq.dim() != 1:
             raise ValueError(f"freq: one dimension, on the GPU, got {list(freq.shape)} on {freq.device}")
-        self.freq, self.rot0, self.layout, self.mscale = freq, rot0, layout, mscale
+        self._freq, self.rot0, self.layout, self.mscale = freq, rot0, layout, mscale
         self.device = freq.device
         self._args = (_on(freq, freq.device, torch.float64, "freq"), 2 * int(freq.numel()), rot0, layout, mscale)
+
+    @property
+    def freq(self) -> torch.Tensor:
+        return self._freq
 
     @staticmethod
     def make(rot: int, device="cuda", rot0: int = 0, layout: int = IDX_ROPE_HALF, **scaling) -> "Rotary":
@@ -604,7 +608,7 @@ class Cache:
             if rows and not scale[:1].is_contiguous():
                 raise ValueError(f"cache scale: a slot's scales follow each other; strides {scale.stride()}")
             ld_scale = scale.stride(0)
-        self.data, self.scale, self.fmt, self.D = data, scale, fmt, D
+        self._data, self._scale, self.fmt, self.D = data, scale, fmt, D
         self.rows, self.H, self.device = rows, H, data.device
         ld = data.stride(0) * (2 if fmt == IDX_K_MXFP4 else 1)
         self._struct = idx_cache(data.data_ptr(), None if scale is None else scale.data_ptr(), rows, ld, ld_scale,
@@ -622,6 +626,15 @@ class Cache:
         elif fmt == IDX_K_MXFP4:
             scale = torch.zeros((rows, H, D // 32), dtype=torch.uint8, device=device)
         return Cache(data, scale, D=D, fmt=fmt)
+
+    # the tensors of a handle stay the ones its struct points to
+    @property
+    def data(self) -> torch.Tensor:
+        return self._data
+
+    @property
+    def scale(self) -> Optional[torch.Tensor]:
+        return self._scale
 
     def struct(self) -> idx_cache:
         return self._struct
@@ -671,6 +684,8 @@ def idx_cache_write(writes, stream=None) -> None:
         if w.rotary is not None:
             keep.append(w.rotary.struct(w.pos, x, w.inverse))
             a.rotary = ctypes.pointer(keep[-1])
+        elif w.pos is not None:
+            raise ValueError("pos without a rotary")
         if w.slot is not None:
             if w.slot.shape != x.shape[:1]:
                 raise ValueError("slot: [T], one slot a row")
@@ -691,7 +706,7 @@ def idx_cache_read(cache: Cache, rows: Optional[torch.Tensor] = None, out: Optio
         at, n = _on(rows, device, torch.int32, "rows"), rows.shape[0]
     with _on_stream(device, stream) as st:
         if out is None:
-            out = cache.data.new_empty((n, cache.H, cache.D), dtype=dtype)
+            out = cache._data.new_empty((n, cache.H, cache.D), dtype=dtype)
         elif out.device != device or out.shape[0] != n:
             raise ValueError(f"out: {n} rows on {device}")
         s = load_library().idx_cache_read(cache._struct, at, _rows(out, "out"), st)

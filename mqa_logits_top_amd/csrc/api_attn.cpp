@@ -17,7 +17,6 @@ constexpr int32_t MAX_D = 512;
 constexpr int32_t MAX_ROT = 512;
 constexpr int32_t MAX_POOL = 64;
 constexpr int64_t MAX_LD = (int64_t)1 << 31;   // strides: their products with 32-bit counts stay inside 64 bits
-
 constexpr int64_t MAX_ROW = (int64_t)1 << 30;  // elements of an attention cache's slot: 32 bits of bytes
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -114,8 +113,15 @@ idx::RowJob row_job(const idx_rows &x, const idx_rotary *r, const int32_t *slot,
   return j;
 }
 
-// Workgroups of a write at 64 lanes a row, the fewest rows to a workgroup: below 2^31.
-bool too_many(const idx_rows &x) { return (int64_t)x.T * x.H >= (int64_t)1 << 31; }
+// Rows that one launch does not reach: a lane to 8 values, fewer than 2^32 lanes.
+bool too_many(const idx_rows &x) {
+  int64_t lanes = 1;
+  while (8 * lanes < x.D) lanes *= 2;
+  return (int64_t)x.T * x.H >= ((int64_t)1 << 31) / lanes;
+}
+
+// The scale for powers of two.
+float scale2_of(const idx_attn *a) { return (float)((double)a->scale * 1.4426950408889634); }
 
 idx_status check_attn(const idx_attn *a) {
   if (!a) return IDX_E_NULL;
@@ -134,7 +140,8 @@ idx_status check_attn(const idx_attn *a) {
   if (a->L < 0 || a->n_sel < 0 || a->ld_sel < 0 || (a->q.T > 1 && a->ld_sel < a->n_sel)) return IDX_E_SHAPE;
   if (!a->slot_of_key && a->L > a->k.rows) return IDX_E_SHAPE;
   if (a->pool < 1 || a->pool > MAX_POOL || (a->pool & (a->pool - 1))) return IDX_E_UNSUPPORTED;
-  if (!std::isfinite(a->scale)) return IDX_E_PARAM;
+  if ((int64_t)a->q.T * a->q.H >= (int64_t)1 << 26) return IDX_E_UNSUPPORTED;   // at most a wave each: 2^32 lanes
+  if (!std::isfinite(scale2_of(a))) return IDX_E_PARAM;
   if ((a->ks == nullptr) != (a->ke == nullptr) || (a->pool > 1 && !a->ks && a->q.T > 0)) return IDX_E_NULL;
   if (a->q.T > 0 && a->n_sel > 0 && !a->sel) return IDX_E_NULL;
   // the attention kernel reads 16 bytes of a cache row at a time
@@ -301,7 +308,7 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
   g.Hq = a->q.H;
   g.Hkv = a->k.H;
   g.G = a->q.H / a->k.H;
-  g.scale2 = (float)((double)a->scale * 1.4426950408889634);
+  g.scale2 = scale2_of(a);
   g.lse = a->lse;
   return launched(idx::launch_attn(g, a->q.dtype, a->k.fmt, a->q.D, plan, ws, (hipStream_t)stream));
 }

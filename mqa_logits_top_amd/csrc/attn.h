@@ -24,8 +24,8 @@ struct AttnArgs {
   const int32_t *table;
   int32_t L;
   int32_t T, Hq, Hkv, G;
-  float scale2;              // scale * log2(e); launch_attn makes it >= 0 ...
-  uint32_t q_sign;           // ... and flips q's signs instead (filled there)
+  float scale2;              // scale * log2(e); launch_attn makes it > 0 ...
+  uint32_t q_sign, q_keep;   // ... and flips q's signs, or zeroes q, instead (filled there)
   float *lse;
   int32_t blocks;            // head blocks of a cache head's G query heads
   int32_t splits;            // workgroups a row's entries are divided over

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
     for (int r = 0; r < 4; ++r) {
       const int64_t e = e_next - CHUNK + 64 * r + lane;
       int64_t key = id[r];
-      if (a.pool_sh) key = (key << a.pool_sh) + win0 + (e & ((1 << a.pool_sh) - 1));
+      if (a.pool_sh) key = (key * (1 << a.pool_sh)) + win0 + (e & ((1 << a.pool_sh) - 1));
       const bool ok = e < e_end && id[r] >= 0 && key >= win0 && key < win1;
       row[r] = ok ? (int32_t)key : -1;
       if (a.table && ok) row[r] = a.table[key];
@@ -227,7 +227,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
     wave_sync();
     if (e_left <= 0 && (tail & (TILE - 1))) {
       const uint32_t last = (tail - 1) & (QUEUE - 1), at = tail + (uint32_t)lane;
-      if (at < ((tail + TILE - 1) & ~(uint32_t)(TILE - 1))) {
+      if ((uint32_t)lane < (-tail & (TILE - 1))) {
         if constexpr (WIDE || FP8) queue[at & (QUEUE - 1)] = queue[last];
         if constexpr (!WIDE) offsets[at & (QUEUE - 1)] = offsets[last];
       }
@@ -250,7 +250,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
       u32x4 w = {0u, 0u, 0u, 0u};
       if (m * 16 + c < heads)
         w = *(const u32x4 *)(a.q + (int64_t)t * a.q_t + (int64_t)(head0 + m * 16 + c) * a.q_h + 2 * e);
-      q[m][s] = w ^ a.q_sign;
+      q[m][s] = (w & a.q_keep) ^ a.q_sign;
     }
 
   f32x4 o[MT][DN];
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float top = max8(sc[m]);
-      if constexpr (!FP8) top *= a.scale2;     // scale2 >= 0: the largest product is the largest dot's
+      if constexpr (!FP8) top *= a.scale2;     // scale2 > 0: the largest product is the largest dot's
       // The reference moves only when a score is 2^8 above it: weights then stay below 2^8, and the
       // accumulators are rescaled a few times a row instead of at most tiles.  The four lanes of a head
       // share their reference, so a lane's own scores decide whether there is anything to do.
@@ -701,7 +701,9 @@ hipError_t launch_attn(AttnArgs &a, int32_t dtype, int32_t fmt, int32_t D, const
   a.part_ml = a.part + (size_t)blocks * heads * D;
   // a negative factor turns q over instead, so that the largest product comes from the largest dot
   a.q_sign = a.scale2 < 0.f ? 0x80008000u : 0u;
-  a.scale2 = std::fabs(a.scale2);
+  // and a factor of zero zeroes q, so that the product of the mask's -inf with it stays -inf
+  a.q_keep = a.scale2 == 0.f ? 0u : ~0u;
+  a.scale2 = a.scale2 == 0.f ? 1.f : std::fabs(a.scale2);
   const bool bf16 = dtype == IDX_K_BF16, fp8 = fmt == IDX_K_FP8_E4M3;
   hipError_t e;
   if (bf16)

@@ -53,6 +53,8 @@ def test_rope_refusals(lib):
     # outputs whose rows share memory, and in place with other strides
     assert rope(o=_rows(data=2 * F, ld_h=0)) == SHAPE and rope(o=_rows(data=2 * F, ld_t=512)) == SHAPE
     assert rope(o=_rows(ld_t=2048)) == SHAPE
+    many = dict(T=2 ** 24, H=8, ld_t=1024)                              # 2^27 rows of 16 lanes
+    assert rope(x=_rows(**many), o=_rows(data=2 * F, **many)) == UNSUPPORTED
     assert rope(x=_rows(T=0, data=None), o=_rows(T=0, data=None)) == OK
     assert rope(x=_rows(H=0, data=None), o=_rows(H=0, data=None)) == OK
 
@@ -110,7 +112,7 @@ def test_attn_refusals(lib):
             (UNSUPPORTED, dict(k=_cache(fmt=FP4), v=_cache(fmt=FP4))),
             (UNSUPPORTED, dict(q=r(D=96), out=r(D=96), k=_cache(D=96), v=_cache(D=96))),
             (UNSUPPORTED, dict(pool=3, ks=F, ke=F)), (UNSUPPORTED, dict(pool=0)), (UNSUPPORTED, dict(pool=128, ks=F, ke=F)),
-            (PARAM, dict(scale=float("inf"))), (NULL, dict(ks=F)), (NULL, dict(pool=8)), (NULL, dict(sel=None)),
+            (UNSUPPORTED, dict(q=r(T=2 ** 25), out=r(T=2 ** 25))), (PARAM, dict(scale=3e38)), (PARAM, dict(scale=float("inf"))), (NULL, dict(ks=F)), (NULL, dict(pool=8)), (NULL, dict(sel=None)),
             (NULL, dict(q=r(data=None))), (ALIGN, dict(sel=F + 2)), (ALIGN, dict(lse=F + 1)),
             (ALIGN, dict(k=_cache(ld=1032), v=_cache(ld=1032))), (ALIGN, dict(ks=F + 1, ke=F)), (ALIGN, dict(slot_of_key=F + 3)), (ALIGN, dict(q=r(data=F + 8)))]:
         assert size(**bad) == status, bad

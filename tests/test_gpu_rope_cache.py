@@ -98,7 +98,7 @@ def test_rope_gradient_is_its_inverse():
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
-@pytest.mark.parametrize("fmt,D", [(FP8, 8), (FP8, 64), (FP8, 72), (FP8, 128), (FP8, 512), (FP4, 32), (FP4, 96),
+@pytest.mark.parametrize("fmt,D", [(FP8, 8), (FP8, 16), (FP8, 24), (FP8, 64), (FP8, 72), (FP8, 128), (FP8, 512), (FP4, 32), (FP4, 96),
                                    (FP4, 128), (FP4, 512)])
 @pytest.mark.parametrize("T,H", [(1, 1), (17, 5)])
 def test_quantised_codes(dtype, fmt, D, T, H):
@@ -299,3 +299,40 @@ def test_indexer_inputs(fmt):
     p.k_scale = kscale.reshape(L) if fmt == FP8 else kscale.reshape(L, -1)
     dq = oracle.Dequantised(p)
     topk_ok(gi.cpu().numpy(), gv.cpu().numpy(), oracle.rows_logits(dq, range(T)), dq.ks, K)
+
+
+def test_debug_mode_finds_a_slot_named_twice(monkeypatch):
+    """IDX_DEBUG: a slot of one array named twice is reported before anything is written; slots outside the
+    cache may repeat."""
+    x, c = _x(1, 5, 1, 64).cuda(), idx.Cache.empty(10, 1, 64)
+    monkeypatch.setenv("IDX_DEBUG", "1")
+    ok = torch.tensor([-1, 3, -1, 99, 99], dtype=torch.int32, device="cuda")
+    idx.idx_cache_write([idx.Write(x, c, slot=ok)])
+    before = c.data.clone()
+    twice = torch.tensor([0, 3, 1, 3, 9], dtype=torch.int32, device="cuda")
+    with pytest.raises(idx.IdxError) as e:
+        idx.idx_cache_write([idx.Write(x, c, slot=ok), idx.Write(x, c, slot=twice)])
+    assert e.value.status == 9
+    assert torch.equal(c.data, before)
+
+
+def test_binding_refusals():
+    """What the binding refuses before the C entry points: shapes, types, devices and leftovers."""
+    plan, c = idx.Rotary.make(64), idx.Cache.empty(8, 2, 128)
+    x, pos = _x(1, 4, 2, 128).cuda(), torch.zeros(4, dtype=torch.int32, device="cuda")
+    bad = [lambda: idx.idx_rope(x, pos.long(), plan), lambda: idx.idx_rope(x, pos[:3], plan),
+           lambda: idx.idx_rope(x, pos.cpu(), plan), lambda: idx.idx_rope(x.cpu(), pos, plan),
+           lambda: idx.idx_rope(x.transpose(1, 2), pos, plan), lambda: idx.idx_rope(x[0], pos, plan),
+           lambda: idx.idx_cache_write([idx.Write(x, c, pos=pos)]),
+           lambda: idx.idx_cache_write([idx.Write(x, c, slot=pos[:2])]),
+           lambda: idx.idx_cache_write([idx.Write(x, c, rotary=plan)]),
+           lambda: idx.idx_cache_read(c, pos.long()), lambda: idx.idx_cache_read(c, pos, out=x[:3]),
+           lambda: idx.Cache(c.data, c.scale[:7]), lambda: idx.Cache(c.data.float(), c.scale),
+           lambda: idx.Cache(c.data.transpose(0, 1), c.scale.transpose(0, 1))]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(idx.IdxError):                     # a cache of other heads
+        idx.idx_cache_write([idx.Write(x[:, :1], c)])
+    with pytest.raises(AttributeError):
+        c.data = x

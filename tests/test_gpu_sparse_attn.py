@@ -76,6 +76,41 @@ def test_list_lengths(T, n, fp8):
     _check(_q(4, T, 8, 128, torch.bfloat16), k, v, _sel(rng, T, n, 3000), 0.1)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T,Hq,n", [(1030, 32, 70), (600, 50, 33), (512, 64, 100)])
+def test_many_rows_of_many_heads(dtype, fp8, D, T, Hq, n):
+    """Rows that fill the machine take 32 heads to a wave."""
+    rng = np.random.default_rng(T)
+    k, v = _caches(21, 400, 1, D, dtype, fp8)
+    s = _sel(rng, T, n, 400, holes=0.1)
+    s[3] = -1
+    s[7, :] = -1
+    s[7, 5] = 11
+    _check(_q(22, T, Hq, D, dtype), k, v, s, D ** -0.5)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,Hkv,n", [(300, 1, 700), (33, 8, 900), (2, 2, 3000), (130, 1, 300)])
+def test_divided_lists(T, Hkv, n, fp8):
+    """Lists divided over workgroups, over waves, and over both; holes and an empty row among them."""
+    rng = np.random.default_rng(n)
+    k, v = _caches(23, 4000, Hkv, 64, torch.bfloat16, fp8)
+    s = _sel(rng, T, n, 4000, holes=0.2)
+    s[1] = -1
+    s[0, : n // 2] = -1
+    _check(_q(24, T, 4 * Hkv, 64, torch.bfloat16), k, v, s, 0.15)
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-30])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_scales_of_any_sign(scale, fp8):
+    rng = np.random.default_rng(3)
+    k, v = _caches(25, 300, 2, 64, torch.float16, fp8)
+    _check(_q(26, 5, 32, 64, torch.float16), k, v, _sel(rng, 5, 200, 300), scale)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T,n", [(6, 70), (40, 515)])
 def test_holes_and_empty_rows(T, n, fp8):
@@ -227,6 +262,82 @@ def test_long_cache_offsets():
     b = idx.idx_sparse_attn(q, near, near, torch.arange(4, dtype=torch.int32, device="cuda").expand(2, 4).contiguous(),
                             0.1)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("T,Hq,fp8", [(1100, 32, False), (1100, 32, True), (2, 16, True)])
+def test_long_cache_offsets_of_one_head(T, Hq, fp8):
+    """The same with many rows of many heads, and with E4M3 codes."""
+    rows, D = (40_000_000 if fp8 else 20_000_000), 128                         # 5.1 GB
+    at = torch.tensor([9, rows // 2, rows // 3, rows - 1], dtype=torch.int32)
+    g = torch.Generator().manual_seed(2)
+    small = idx.Cache.empty(4, 1, D, FP8 if fp8 else idx.IDX_K_BF16)
+    idx.idx_cache_write([idx.Write(torch.randn((4, 1, D), generator=g).to(torch.bfloat16).cuda(), small)])
+    data = torch.zeros((rows, 1, D), dtype=small.data.dtype, device="cuda")
+    scale = torch.zeros((rows, 1), device="cuda") if fp8 else None
+    big = idx.Cache(data, scale, fmt=small.fmt)
+    data[at.long().cuda()] = small.data
+    if fp8:
+        scale[at.long().cuda()] = small.scale
+    q = _q(3, T, Hq, D, torch.bfloat16).cuda()
+    sel = torch.arange(4, dtype=torch.int32).expand(T, 4).contiguous()
+    a = idx.idx_sparse_attn(q, big, big, at.expand(T, 4).contiguous().cuda(), 0.1)
+    b = idx.idx_sparse_attn(q, small, small, sel.cuda(), 0.1)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_refusals():
+    """What the binding and the C entry point refuse."""
+    k, v = _caches(1, 20, 2, 64, torch.bfloat16, False)
+    q, s = _q(1, 3, 4, 64, torch.bfloat16).cuda(), torch.zeros((3, 5), dtype=torch.int32, device="cuda")
+    w = torch.zeros(3, dtype=torch.int32, device="cuda")
+    f8 = idx.Cache.empty(20, 2, 64)
+    for bad in (lambda: idx.idx_sparse_attn(q, k, v, s.long(), 0.1), lambda: idx.idx_sparse_attn(q, k, v, s[:2], 0.1),
+                lambda: idx.idx_sparse_attn(q, k, v, s.cpu(), 0.1), lambda: idx.idx_sparse_attn(q.cpu(), k, v, s, 0.1),
+                lambda: idx.idx_sparse_attn(q, k, v, s, 0.1, ks=w), lambda: idx.idx_sparse_attn(q, k, v, s.t(), 0.1),
+                lambda: idx.idx_sparse_attn(q, k, v, s, 0.1, ks=w, ke=w[:2]),
+                lambda: idx.idx_sparse_attn(q, k, v, s, 0.1, slot_of_key=w.long()),
+                lambda: idx.idx_sparse_attn(q, k, v, s, 0.1, lse=torch.zeros(3, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: idx.idx_sparse_attn(q[:, :3], k, v, s, 0.1), lambda: idx.idx_sparse_attn(q.half(), k, v, s, 0.1),
+                lambda: idx.idx_sparse_attn(q, k, f8, s, 0.1), lambda: idx.idx_sparse_attn(q, k, v, s, 0.1, pool=8),
+                lambda: idx.idx_sparse_attn(q.float(), k, v, s, 0.1),
+                lambda: idx.idx_sparse_attn(q, k, v, s, float("nan"))):
+        with pytest.raises(idx.IdxError):
+            bad()
+
+
+def test_debug_mode_checks_windows(monkeypatch):
+    k, v = _caches(1, 20, 1, 64, torch.bfloat16, False)
+    q, s = _q(1, 2, 4, 64, torch.bfloat16).cuda(), torch.zeros((2, 5), dtype=torch.int32, device="cuda")
+    w = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("IDX_DEBUG", "1")
+    idx.idx_sparse_attn(q, k, v, s, 0.1, ks=w(0, 3), ke=w(20, 3))
+    with pytest.raises(idx.IdxError) as e:
+        idx.idx_sparse_attn(q, k, v, s, 0.1, ks=w(0, 4), ke=w(21, 5))
+    assert e.value.status == 9
+
+
+def test_two_graphs_beside_each_other():
+    """Two captured calls with workspaces of their own, replayed in turn and between eager calls."""
+    rng = np.random.default_rng(8)
+    k, v = _caches(27, 5000, 1, 128, torch.bfloat16, True)
+    calls = []
+    for i in range(2):
+        q, s = _q(30 + i, 1, 16, 128, torch.bfloat16).cuda(), torch.from_numpy(_sel(rng, 1, 2048, 5000)).cuda()
+        want = [x.clone() for x in idx.idx_sparse_attn(q, k, v, s, 0.09)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = idx.idx_sparse_attn(q, k, v, s, 0.09)
+        calls.append((g, out, want, q, s))
+    for turn in range(4):
+        for g, out, want, _, _ in calls:
+            out[0].fill_(3)
+            g.replay()
+        idx.idx_sparse_attn(calls[0][3], k, v, calls[1][4], 0.3)
+        torch.cuda.synchronize()
+        for g, out, want, _, _ in calls:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
 def test_repeatable_and_other_streams():
