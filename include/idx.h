@@ -351,7 +351,7 @@ typedef struct idx_rows {
  * to the output's type. */
 enum { IDX_ROPE_HALF = 0, IDX_ROPE_INTERLEAVED = 1 };
 typedef struct idx_rotary {
-  const double *freq;   /* [rot / 2] radians a position (idx_rope_freqs)        */
+  const double *freq;   /* [rot / 2] radians a position (idx_rope_freqs), within +-2 */
   const int32_t *pos;   /* [T] position of each row, any sign                   */
   int32_t rot, rot0;    /* multiples of 8, 8 <= rot, rot0 + rot <= D            */
   int32_t layout;       /* IDX_ROPE_HALF or IDX_ROPE_INTERLEAVED                */
@@ -430,9 +430,10 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
  * twice.  Rows that do not count are not read, so what they hold reaches no output.  The order of
  * entries has no influence beyond the rounding of sums; results are bitwise repeatable.
  * q and out share type and sizes, IDX_K_BF16 or IDX_K_F16; the caches are of that type or E4M3, both
- * alike, with the same slots and strides; D = 64 or 128.  Products run on the matrix cores with fp32 accumulation, E4M3 codes
- * converted exactly; T * Hq below 2^26; weights are rounded to 16 bits before the second product (2^-9 relative in
- * bf16, 2^-12 in fp16: bf16 wherever v is E4M3), sums and maxima are fp32.
+ * alike, with the same slots and strides; D = 64 or 128; T * Hq below 2^26.  Products run on the matrix
+ * cores with fp32 accumulation, E4M3 codes converted exactly; weights are rounded before the second
+ * product (relative, at most 2^-8 in bf16, 2^-11 in fp16, 2^-16 for fp16 with E4M3 caches), sums and
+ * maxima are fp32.
  * ws: idx_sparse_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap
  * in time need one each. */
 typedef struct idx_attn {

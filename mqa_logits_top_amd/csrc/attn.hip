@@ -137,7 +137,8 @@ constexpr int wave_lds(bool fp8, int D, bool wide) {
 // MT = 1 may run several waves a workgroup, which divide the entries and join through LDS.
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(AttnArgs a) {
-  constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
+  constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range ...
+  constexpr bool TWO = FP8 && !BF16;      // ... and for an fp16 result two parts, 16 bits of precision
   constexpr int KS = D / 32;              // steps of the first product
   constexpr int DN = D / 16;              // tiles of the second product
   constexpr int HEADS = MT * 16;
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
         for (int i = 0; i < 8; ++i)
           if (8 * g + i >= n) sc[m][i] = NEG_INF;
     }
-    u32x4 p[MT];
+    u32x4 p[MT], rest[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       float top = max8(sc[m]);
@@ -422,6 +423,8 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
           y *= vsc[2 * i + 1];
         }
         p[m][i] = pack2<PV_BF16>(x, y);
+        if constexpr (TWO)
+          rest[m][i] = pack2<PV_BF16>(x - __uint_as_float(p[m][i] << 16), y - __uint_as_float(p[m][i] & 0xFFFF0000u));
       }
     }
 
@@ -475,7 +478,10 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int d = 0; d < DN; ++d) o[m][d] = mfma<PV_BF16>(vt[d], p[m], o[m][d]);
+      for (int d = 0; d < DN; ++d) {
+        o[m][d] = mfma<PV_BF16>(vt[d], p[m], o[m][d]);
+        if constexpr (TWO) o[m][d] = mfma<PV_BF16>(vt[d], rest[m], o[m][d]);
+      }
   }
 
   copies_left<0>();   // none may write LDS that is another wave's by then

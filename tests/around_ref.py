@@ -91,7 +91,7 @@ def attend(q, k, v, rows, scale, weight_step, dtype):
     The bounds: a score is a sum of D exact products in fp32 (D + 2 roundings of 2^-24 of the products'
     magnitudes, once more for the scales), off by ds; weights are exp of it, off by 2 ds where the
     normalisation moves with them, plus 2^-21 for the exponential, its argument's rounding (2^-23 of the
-    largest score's distance, within ds) and the reciprocal; each weight is rounded to 16 bits
+    largest score's distance, within ds) and the reciprocal; each weight is rounded
     (weight_step: half a step; fp16 weights below its smallest normal lose up to 2^-25 of the largest);
     sums over n keys add n 2^-23; the result is rounded to the output's type."""
     T, Hq, D = q.shape

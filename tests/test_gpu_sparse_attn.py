@@ -34,7 +34,8 @@ def _check(q, k, v, sel, scale, pool=1, ks=None, ke=None, table=None, **kw):
     out, lse = idx.idx_sparse_attn(q.cuda(), k, v, cu(sel), scale, pool=pool, ks=cu(ks), ke=cu(ke),
                                    slot_of_key=cu(table), **kw)
     rows = keys_of(np.asarray(sel), ks, ke, pool, k.rows if table is None else len(table), table, k.rows)
-    step = 2.0 ** -8 if q.dtype == torch.bfloat16 or k.fmt == FP8 else 2.0 ** -11
+    # fp16 with E4M3 caches: weights in two bf16 parts, the second's half step of what the first left
+    step = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -16 if k.fmt == FP8 else 2.0 ** -11
     want, wl, bo, bl = attend(q.double().numpy(), _values(k), _values(v), rows, scale, step, q.dtype)
     got, gl = out.cpu().double().numpy(), lse.cpu().double().numpy()
     assert np.array_equal(np.isneginf(gl), np.isneginf(wl))
