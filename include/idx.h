@@ -346,9 +346,8 @@ typedef struct idx_rows {
  * and turned back by it when `inverse` is set (the transpose: what a gradient, or a key
  * that moves to another position, needs).  IDX_ROPE_HALF pairs dims rot0 + i and
  * rot0 + rot/2 + i, IDX_ROPE_INTERLEAVED dims rot0 + 2 i and rot0 + 2 i + 1.  Angles are
- * computed and reduced in fp64 for any int32 position; cosine and sine are rounded to fp32,
- * their products and sum kept in fp64, and the result rounded once to fp32 and once more
- * to the output's type. */
+ * reduced and turned in fp64 for any int32 position; the result is rounded to fp32 and once
+ * more to the output's type. */
 enum { IDX_ROPE_HALF = 0, IDX_ROPE_INTERLEAVED = 1 };
 typedef struct idx_rotary {
   const double *freq;   /* [rot / 2] radians a position (idx_rope_freqs), within +-2 */
@@ -395,8 +394,8 @@ typedef struct idx_cache {
 
 /* One array of rows on its way into a cache: row (t, h) of x, rotated if `rotary` is not NULL, is
  * quantised and stored to slot slot[t] (t itself where slot is NULL).  E4M3: amax the row's largest
- * magnitude, scale = amax / 448 and code = x * (448 / amax) in fp32, rounded to nearest even (a row
- * with amax < 2^-100: zeros, scale 1).  MXFP4: exponent floor(log2 amax) - 2 of each 32 values,
+ * magnitude, scale = amax / 448 in fp32 and code = x * 448 / amax, rounded to fp32 and then to nearest
+ * even (a row with amax < 2^-100: zeros, scale 1).  MXFP4: exponent floor(log2 amax) - 2 of each 32 values,
  * codes rounded to nearest even and saturating at 6 (a block with amax < 2^-100: zeros, E8M0 code
  * 0).  The other formats round to nearest even. */
 typedef struct idx_write {

@@ -109,6 +109,17 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *v) {
   return (uint32_t)w;
 }
 
+template <int LANE>   // x of that lane of the quad
+__device__ __forceinline__ float of_quad(float x) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), LANE * 0x55, 0xF, 0xF, false));
+}
+// 448 / amax less its rounded value inv: with it x * 448 / amax is rounded once, so that values half way between
+// two codes (16-bit values often are) go to the even one.  One more fma a value (no time); 0.1% of a bf16 array's codes
+// would go to the other one without it.
+__device__ __forceinline__ float inverse_rest(float amax, float inv) {
+  return __builtin_fmaf(-inv, amax, 448.0f) * (inv * (1.0f / 448.0f));
+}
+
 // Sine and cosine of an angle below 2^32, within a few 2^-50: the angle less its nearest multiple of pi/2
 // (pi/2 in three parts of 53 bits; each fma is exact but for its one rounding, and the angle's multiple k of
 // pi/2 is below 2^32), then the Taylor series of sine and cosine on [-pi/4, pi/4] (terms dropped: below
@@ -141,8 +152,7 @@ __device__ __forceinline__ void sin_cos(double x, double *sn, double *cs) {
   *cs = (q + 1u) & 2u ? -b : b;
 }
 
-// The lane's four pairs: (v[e], v[4 + e]) for split halves, else neighbours.  In fp64 the products of the
-// fp32 factors are exact, so each result is rounded once.
+// The lane's four pairs: (v[e], v[4 + e]) for split halves, else neighbours.  In fp64, each result rounded once.
 template <bool SPLIT>
 __device__ __forceinline__ void rotate4(float *v, const double *cs, const double *sn) {
 #pragma unroll
@@ -190,15 +200,15 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
     const int h = hs + i * j.groups;
     if (live && h < j.H) raw[i] = load8<F32>(xt + (int64_t)h * j.x_h, j.dtype, e0, e1, split);
   }
-  double cs[4], sn[4];           // rounded to fp32
+  double cs[4], sn[4];
   if (turned) {
     const double p = (double)j.pos[t], gain_s = j.inverse ? -j.mscale : j.mscale;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       double s, k;
       sin_cos(p * j.freq[part / 2 + i], &s, &k);
-      cs[i] = (double)(float)(k * j.mscale);
-      sn[i] = (double)(float)(s * gain_s);
+      cs[i] = k * j.mscale;
+      sn[i] = s * gain_s;
     }
   }
   float v[HEADS][8];
@@ -235,7 +245,7 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
     const int mine = c & 3;
     const uint32_t ml = mine & 2 ? (mine & 1 ? m[3] : m[2]) : (mine & 1 ? m[1] : m[0]);
     const float amax = __uint_as_float(ml);
-    const float inv = ml >= TINY ? 448.0f / amax : 0.f;
+    const float inv = ml >= TINY ? 448.0f / amax : 0.f, more = inverse_rest(amax, inv);
     if (sh >= 2) {
       // a NaN or an infinity in the row makes the scale NaN, and with it the whole row
       const int h = hs + mine * j.groups;
@@ -243,26 +253,24 @@ __global__ __launch_bounds__(THREADS) void write_kernel(RowJobs jobs) {
         *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
             ml >= INF ? __uint_as_float(0x7FC00000u) : ml >= TINY ? amax / 448.0f : 1.0f;
     }
-    const float quad[HEADS] = {
-        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0x00, 0xF, 0xF, false)),
-        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0x55, 0xF, 0xF, false)),
-        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0xAA, 0xF, 0xF, false)),
-        __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(inv), 0xFF, 0xF, 0xF, false))};
+    const float quad[HEADS] = {of_quad<0>(inv), of_quad<1>(inv), of_quad<2>(inv), of_quad<3>(inv)};
+    const float rest[HEADS] = {of_quad<0>(more), of_quad<1>(more), of_quad<2>(more), of_quad<3>(more)};
 #pragma unroll
     for (int i = 0; i < HEADS; ++i) {
       const int h = hs + i * j.groups;
       if (h >= j.H) break;
-      float f = quad[i];
+      float f = quad[i], f1 = rest[i];
       if (sh < 2) {   // rows of one or two lanes: no quad of their own
         const float am = __uint_as_float(m[i]);
         f = m[i] >= TINY ? 448.0f / am : 0.f;
+        f1 = inverse_rest(am, f);
         if (c == 0)
           *(float *)(j.scale + slot * j.scale_t + (int64_t)h * j.scale_h) =
               m[i] >= INF ? __uint_as_float(0x7FC00000u) : m[i] >= TINY ? am / 448.0f : 1.0f;
       }
       float y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = v[i][e] * f;
+      for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(v[i][e], f, v[i][e] * f1);
       if (live) {
         uint8_t *o = out + (int64_t)h * j.out_h;
         const uint32_t w0 = e4m3x4(y), w1 = e4m3x4(y + 4);

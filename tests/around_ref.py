@@ -29,8 +29,8 @@ def rotate(x: np.ndarray, pos: np.ndarray, freq: np.ndarray, rot0: int, half: bo
 
 
 def rotate_bound(want: np.ndarray, mag: np.ndarray, dtype) -> np.ndarray:
-    """Cosine and sine are rounded to fp32 (2^-24 each, on the pair's magnitudes; 2^-23 covers the fp64
-    angle as well), the sum to fp32 (2^-24) and to the output's type (half a step)."""
+    """The angle and its cosine and sine, in fp64, are off by less than 2^-23 on the pair's magnitudes; the sum is
+    rounded to fp32 (2^-24) and to the output's type (half a step)."""
     return (HALF_STEP[dtype] + 2.0 ** -23) * np.abs(want) + 2.0 ** -23 * mag + SMALLEST[dtype]
 
 
@@ -39,10 +39,10 @@ def quantise_e4m3(x: np.ndarray):
     x = np.asarray(x, np.float32)
     amax = np.abs(x).max(-1)
     some = amax >= np.float32(2.0 ** -100)
-    with np.errstate(divide="ignore"):
-        inv = np.where(some, np.float32(448) / amax, np.float32(0)).astype(np.float32)
     scale = np.where(some, amax / np.float32(448), np.float32(1)).astype(np.float32)
-    y = (x * inv[..., None]).astype(np.float32)
+    with np.errstate(invalid="ignore"):
+        y = x.astype(np.float64) * 448 / np.where(some, amax, np.inf)[..., None].astype(np.float64)
+    y = y.astype(np.float32)
     return synth.encode_e4m3(y.astype(np.float64)), scale
 
 
