@@ -32,7 +32,7 @@ struct AttnArgs {
   int32_t waves;             // waves of a workgroup, over which its share is divided
   int64_t per;               // entries of a wave
   // splits > 1: per (row, cache head, head block, split) the unnormalised out of the split's
-  // heads [heads][D], then all their (maximum, sum) pairs
+  // heads [heads][D], then all their (reference, sum, divisor, 0)
   float *part;
   float *part_ml;
 };

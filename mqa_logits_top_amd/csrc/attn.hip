@@ -7,7 +7,10 @@
 //   O^T += V^T P^T: B = P^T, lane l holds head l % 16 and 8 of the 32 keys.  The product sums over keys, so
 //     their order is free: with positions 8 g + 4 h + j for the keys 4 g + j of the h-th 16, the two S^T
 //     results, exponentiated, are the operand as they stand.  A = V^T comes transposed out of LDS.
-// The softmax is the running one: a reference near the maximum, the sum, the unnormalised output.
+// The softmax is the running one: a reference near the maximum, the sum, the unnormalised output.  The weights
+// of the second product are rounded to 16 bits; the output is divided by the sum of the rounded ones (a product
+// with ones), so that a row whose weight lies on few keys gains little error from it.  E4M3 caches put a key's
+// scale into its weight, whose rounding has no such sum: there weights are two 16-bit parts (TWO).
 // Cache rows reach LDS by memory-to-LDS copies that each bring whole rows, K for the next step while this one
 // multiplies, V while the next one's scores are computed.  Waves of the 2000 rows that are resident at once
 // walk their ascending lists at the same pace, so each XCD's L2 meets a row's neighbours' keys soon after.
@@ -138,7 +141,11 @@ constexpr int wave_lds(bool fp8, int D, bool wide) {
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(AttnArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range ...
-  constexpr bool TWO = FP8 && !BF16;      // ... and for an fp16 result two parts, 16 bits of precision
+  // ... and two parts of 8 bits: an fp16 result needs them, and a wave of 16 heads has the time (40 rows x 8 cache
+  // heads: 52.8 us, 52.6 with one part).  With 32 heads a bf16 result has one part: 62 us, 73 with two (2048 rows x
+  // 64 heads x 512 keys); it errs by 1.4 of its own rounding.
+  constexpr bool TWO = FP8 && (!BF16 || MT == 1);
+  constexpr uint32_t ONES = BF16 ? 0x3F803F80u : 0x3C003C00u;
   constexpr int KS = D / 32;              // steps of the first product
   constexpr int DN = D / 16;              // tiles of the second product
   constexpr int HEADS = MT * 16;
@@ -254,13 +261,14 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
       q[m][s] = (w & a.q_keep) ^ a.q_sign;
     }
 
-  f32x4 o[MT][DN];
+  f32x4 o[MT][DN], rounded[MT];           // rounded: sum of the weights as the second product has them
   float ref[MT], neg[MT], sum[MT];        // neg: -ref, or 0 while there is none
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     ref[m] = NEG_INF;
     neg[m] = 0.f;
     sum[m] = 0.f;
+    rounded[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < DN; ++n) o[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -402,6 +410,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
         const float to = __builtin_fmaxf(ref[m], head_max(top));
         const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
         sum[m] *= f;
+        rounded[m] *= f;
 #pragma unroll
         for (int d = 0; d < DN; ++d) o[m][d] *= f;
         ref[m] = to;
@@ -476,12 +485,14 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
                       codes2<true, true>(vt[d][1])};
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
+      if constexpr (!FP8) rounded[m] = mfma<BF16>(u32x4{ONES, ONES, ONES, ONES}, p[m], rounded[m]);
 #pragma unroll
       for (int d = 0; d < DN; ++d) {
         o[m][d] = mfma<PV_BF16>(vt[d], p[m], o[m][d]);
         if constexpr (TWO) o[m][d] = mfma<PV_BF16>(vt[d], rest[m], o[m][d]);
       }
+    }
   }
 
   copies_left<0>();   // none may write LDS that is another wave's by then
@@ -490,37 +501,36 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
     if (a.waves > 1) {
       // each wave's output, sum and reference through LDS; quads of dims exchanged against bank conflicts
       constexpr int QUADS = D / 4;
-      float *const ml = (float *)(lds + a.waves * WAVE_LDS);    // [waves][2][16]
+      float *const ml = (float *)(lds + a.waves * WAVE_LDS);    // [waves][3][16]
       const float l = head_sum(sum[0]);
 #pragma unroll
       for (int d = 0; d < DN; ++d)
         *(f32x4 *)(kbuf + c * D * 4 + ((4 * d + g) ^ (c & 7)) * 16) = o[0][d];
       if (g == 0) {
-        ml[wave * 32 + c] = ref[0];
-        ml[wave * 32 + 16 + c] = l;
+        ml[wave * 48 + c] = ref[0];
+        ml[wave * 48 + 16 + c] = l;
+        ml[wave * 48 + 32 + c] = FP8 ? l : rounded[0][0];
       }
       __syncthreads();
       for (int x = threadIdx.x; x < heads * QUADS; x += 64 * a.waves) {
         const int h = x / QUADS, y = x % QUADS;
         float top = NEG_INF;
-        for (int w = 0; w < a.waves; ++w) top = __builtin_fmaxf(top, ml[w * 32 + h]);
+        for (int w = 0; w < a.waves; ++w) top = __builtin_fmaxf(top, ml[w * 48 + h]);
         const float base = top == NEG_INF ? 0.f : top;
-        float total = 0.f;
+        float total = 0.f, div = 0.f;
         f32x4 r = {0.f, 0.f, 0.f, 0.f};
         for (int w = 0; w < a.waves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(ml[w * 32 + h] - base);
-          total += f * ml[w * 32 + 16 + h];
+          const float f = __builtin_amdgcn_exp2f(ml[w * 48 + h] - base);
+          total += f * ml[w * 48 + 16 + h];
+          div += f * ml[w * 48 + 32 + h];
           r += f * *(const f32x4 *)(lds + w * WAVE_LDS + h * D * 4 + (y ^ (h & 7)) * 16);
         }
         if (a.splits > 1) {
           const int64_t at = (int64_t)blockIdx.x * HEADS + h;
           *(f32x4 *)(a.part + at * D + 4 * y) = r;
-          if (y == 0) {
-            a.part_ml[2 * at] = top;
-            a.part_ml[2 * at + 1] = total;
-          }
+          if (y == 0) *(f32x4 *)(a.part_ml + 4 * at) = f32x4{top, total, div, 0.f};
         } else {
-          r *= finish(total);
+          r *= finish(div);
           *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)(head0 + h) * a.out_h + 8 * y) =
               make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
           if (y == 0 && a.lse) a.lse[(int64_t)t * a.Hq + head0 + h] = lse_of(top, total);
@@ -532,19 +542,16 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
   // lane l holds head l % 16 and dims 16 d + 4 g + j
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const float l = head_sum(sum[m]);
+    const float l = head_sum(sum[m]), div = FP8 ? l : rounded[m][0];
     const int h = m * 16 + c;
     if (a.splits > 1) {
       if (h >= heads) continue;
       const int64_t at = (int64_t)blockIdx.x * HEADS + h;
-      if (g == 0) {
-        a.part_ml[2 * at] = ref[m];
-        a.part_ml[2 * at + 1] = l;
-      }
+      if (g == 0) *(f32x4 *)(a.part_ml + 4 * at) = f32x4{ref[m], l, div, 0.f};
 #pragma unroll
       for (int d = 0; d < DN; ++d) *(f32x4 *)(a.part + at * D + 16 * d + 4 * g) = o[m][d];
     } else {
-      const float f = finish(l);
+      const float f = finish(div);
 #pragma unroll
       for (int d = 0; d < DN; ++d)
         *(uint2 *)(kbuf + h * 2 * D + (((2 * d + (g >> 1)) ^ (h & (OUT_CH - 1))) << 4) + 8 * (g & 1)) =
@@ -572,23 +579,24 @@ __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEA
   constexpr int QUADS = D / 4, GROUPS = MERGE / QUADS;
   __shared__ __attribute__((aligned(16))) float acc[GROUPS][D];
   __shared__ float factor[MAX_SPLITS];
-  __shared__ float shared[2];
+  __shared__ float shared[3];
   const uint32_t th = blockIdx.x;
   const int t = (int)(th / (uint32_t)a.Hq), hq = (int)(th % (uint32_t)a.Hq);
   const int kvh = hq / a.G, in = hq % a.G;
   const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS;
   const int64_t at0 = ((((int64_t)t * a.Hkv + kvh) * a.blocks + in / HEADS) * a.splits) * HEADS + in % HEADS;
   if (threadIdx.x < 64) {   // one wave: every split's reference and sum at once
-    float m[MAX_SPLITS / 64], l[MAX_SPLITS / 64];
+    float m[MAX_SPLITS / 64], l[MAX_SPLITS / 64], div[MAX_SPLITS / 64];
 #pragma unroll
     for (int i = 0; i < MAX_SPLITS / 64; ++i) {
       const int s = threadIdx.x + 64 * i;
       m[i] = NEG_INF;
-      l[i] = 0.f;
+      l[i] = div[i] = 0.f;
       if (s < a.splits) {
-        const float2 ml = *(const float2 *)(a.part_ml + 2 * (at0 + (int64_t)s * HEADS));
-        m[i] = ml.x;
-        l[i] = ml.y;
+        const f32x4 ml = *(const f32x4 *)(a.part_ml + 4 * (at0 + (int64_t)s * HEADS));
+        m[i] = ml[0];
+        l[i] = ml[1];
+        div[i] = ml[2];
       }
     }
     float top = m[0];
@@ -596,7 +604,7 @@ __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEA
     for (int i = 1; i < MAX_SPLITS / 64; ++i) top = __builtin_fmaxf(top, m[i]);
     top = wave_reduce_f32(top, [](float x, float y) { return __builtin_fmaxf(x, y); });
     const float ref = top == NEG_INF ? 0.f : top;
-    float total = 0.f;
+    float total = 0.f, divide = 0.f;
 #pragma unroll
     for (int i = 0; i < MAX_SPLITS / 64; ++i) {
       const int s = threadIdx.x + 64 * i;
@@ -604,12 +612,15 @@ __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEA
       if (s < a.splits) {
         factor[s] = f;
         total += f * l[i];
+        divide += f * div[i];
       }
     }
     total = wave_reduce_f32(total, [](float x, float y) { return x + y; });
+    divide = wave_reduce_f32(divide, [](float x, float y) { return x + y; });
     if (threadIdx.x == 0) {
       shared[0] = top;
       shared[1] = total;
+      shared[2] = divide;
     }
   }
   __syncthreads();
@@ -621,7 +632,7 @@ __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEA
   if (gr) return;
 #pragma unroll
   for (int x = 1; x < GROUPS; ++x) r += *(const f32x4 *)&acc[x][d];
-  r *= finish(shared[1]);
+  r *= finish(shared[2]);
   *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)hq * a.out_h + 2 * d) =
       make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
   if (d == 0 && a.lse) a.lse[th] = lse_of(shared[0], shared[1]);
@@ -629,7 +640,7 @@ __global__ __launch_bounds__(MERGE) void merge_splits_kernel(AttnArgs a, int HEA
 
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 hipError_t launch_width(const AttnArgs &a, unsigned blocks, hipStream_t s) {
-  const size_t lds = (size_t)a.waves * wave_lds(FP8, D, WIDE) + (a.waves > 1 ? 128 * a.waves : 0);
+  const size_t lds = (size_t)a.waves * wave_lds(FP8, D, WIDE) + (a.waves > 1 ? 192 * a.waves : 0);
   hipLaunchKernelGGL((attn_kernel<BF16, FP8, D, MT, WIDE>), dim3(blocks), dim3(64 * a.waves), lds, s, a);
   return hipGetLastError();
 }
@@ -679,7 +690,7 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries
   }
   const int64_t parts = (int64_t)p.waves * p.splits;
   p.per = ((tiles + parts - 1) / parts) * TILE;
-  p.bytes = p.splits > 1 ? (size_t)items * p.splits * heads * (D + 2) * 4 : 0;
+  p.bytes = p.splits > 1 ? (size_t)items * p.splits * heads * (D + 4) * 4 : 0;
   return p;
 }
 
