@@ -154,7 +154,12 @@ idx_status check_attn(const idx_attn *a) {
 }
 
 idx::AttnPlan plan_of(const idx_attn *a) {
-  return idx::plan_attn(a->q.T, a->k.H, a->q.H / a->k.H, a->q.D, (int64_t)a->n_sel * a->pool);
+  const bool fp8 = a->k.fmt == IDX_K_FP8_E4M3;
+  const int64_t entries = (int64_t)a->n_sel * a->pool;
+  // T * entries stays inside 64 bits: 2^26 rows of 2^37
+  const int64_t slots = entries * a->q.T < a->k.rows ? entries * a->q.T : a->k.rows;
+  const int64_t touched = 2 * slots * (int64_t)a->k.H * a->k.D * (fp8 ? 1 : 2);
+  return idx::plan_attn(a->q.T, a->k.H, a->q.H / a->k.H, a->q.D, fp8, entries, touched);
 }
 
 }  // namespace

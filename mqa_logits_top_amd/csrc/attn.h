@@ -44,7 +44,8 @@ struct AttnPlan {
   int64_t per;
   size_t bytes;              // workspace
 };
-AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries);
+// entries: of a list; touched: bytes of the caches that the lists can name at most
+AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64_t entries, int64_t touched);
 hipError_t launch_attn(AttnArgs &a, int32_t dtype, int32_t fmt, int32_t D, const AttnPlan &plan, void *ws,
                        hipStream_t s);
 

@@ -29,6 +29,7 @@ constexpr int CHUNK = 256;    // list entries resolved at a time
 constexpr int QUEUE = 512;    // rows waiting: under two tiles when a chunk is added
 constexpr int MAX_WAVES = 8;  // of a workgroup
 constexpr int MAX_SPLITS = 256;
+constexpr int64_t FROM_MEMORY = (int64_t)128 << 20;   // bytes: half of the last cache
 constexpr float NEG_INF = -__builtin_inff();
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -170,13 +171,21 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
 
   const int lane = threadIdx.x & 63;
   const int c = lane & 15, g = lane >> 4;
-  uint32_t item = blockIdx.x;
-  const int split = (int)(item % (uint32_t)a.splits);
-  item /= (uint32_t)a.splits;
-  const int hb = (int)(item % (uint32_t)a.blocks);
-  item /= (uint32_t)a.blocks;
-  const int kvh = (int)(item % (uint32_t)a.Hkv);
-  const int t = (int)(item / (uint32_t)a.Hkv);
+  // Workgroup b runs on XCD b % 8.  Those that read the same lines share one: the head blocks of a row's part, and
+  // for E4M3, whose rows of 64 bytes and scales share lines, its cache heads too (40 rows x 8 cache heads of 64
+  // dims, 2048 keys: 28 us, 42 without).  Other cache heads keep XCDs of their own, whose L2 holds more rows then
+  // (1023 rows x 2 cache heads of 64 dims: 22.8 us, 24.3 together).
+  const uint32_t kvs = FP8 ? 1u : (uint32_t)a.Hkv, same = (uint32_t)(a.Hkv * a.blocks) / kvs;
+  const uint32_t parts = (uint32_t)a.T * kvs * (uint32_t)a.splits, even = parts & ~7u;
+  const bool last = blockIdx.x >= even * same;                 // one of the parts behind the last multiple of 8
+  const uint32_t i = last ? blockIdx.x - even * same : blockIdx.x >> 3;
+  uint32_t part_of = last ? even + i / same : i / same * 8 + (blockIdx.x & 7u);
+  const uint32_t member = i % same;
+  const int split = (int)(part_of % (uint32_t)a.splits);
+  part_of /= (uint32_t)a.splits;
+  const int t = (int)(part_of / kvs), hb = (int)(member % (uint32_t)a.blocks);
+  const int kvh = FP8 ? (int)(member / (uint32_t)a.blocks) : (int)(part_of % kvs);
+  const int64_t item = (((int64_t)t * a.Hkv + kvh) * a.blocks + hb) * a.splits + split;
   const int head0 = kvh * a.G + hb * HEADS;                    // first query head
   const int heads = min(HEADS, a.G - hb * HEADS);
 
@@ -526,7 +535,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
           r += f * *(const f32x4 *)(lds + w * WAVE_LDS + h * D * 4 + (y ^ (h & 7)) * 16);
         }
         if (a.splits > 1) {
-          const int64_t at = (int64_t)blockIdx.x * HEADS + h;
+          const int64_t at = item * HEADS + h;
           *(f32x4 *)(a.part + at * D + 4 * y) = r;
           if (y == 0) *(f32x4 *)(a.part_ml + 4 * at) = f32x4{top, total, div, 0.f};
         } else {
@@ -546,7 +555,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, 2) void attn_kernel(
     const int h = m * 16 + c;
     if (a.splits > 1) {
       if (h >= heads) continue;
-      const int64_t at = (int64_t)blockIdx.x * HEADS + h;
+      const int64_t at = item * HEADS + h;
       if (g == 0) *(f32x4 *)(a.part_ml + 4 * at) = f32x4{ref[m], l, div, 0.f};
 #pragma unroll
       for (int d = 0; d < DN; ++d) *(f32x4 *)(a.part + at * D + 16 * d + 4 * g) = o[m][d];
@@ -660,7 +669,7 @@ hipError_t launch_dim(const AttnArgs &a, int D, int tiles, unsigned blocks, hipS
 
 }  // namespace
 
-AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries) {
+AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64_t entries, int64_t touched) {
   AttnPlan p{};
   const int64_t tiles = entries > 0 ? (entries + TILE - 1) / TILE : 1;
   // 32 heads to a wave where rows alone fill the machine (2 waves a SIMD): each key is fetched once for them
@@ -682,11 +691,17 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, int64_t entries
       // keys: 15.9 us, 17.3 with one wave
       while (p.waves < MAX_WAVES && p.waves < tiles && items * p.waves < 1024) p.waves *= 2;
     }
+  } else if (p.tiles == 1 && items <= 384 && tiles > 32 && touched > FROM_MEMORY) {
+    // Rows that come from memory are read at its rate only if every CU asks for its share, which 320 workgroups of
+    // four waves on 256 CUs do not: 40 rows x 8 cache heads of a 330 MB cache, 2048 keys: 53 us, 63 that way
+    while (items * p.splits < 1024) p.splits *= 2;
   } else if (p.tiles == 1) {
-    // whole workgroups no longer spread evenly over 256 CUs (40 rows x 8 cache heads, 2048 keys: 50 us, 66 with
-    // four waves to a workgroup), and a short list is not worth the join (64 rows x 8 cache heads, 512 keys: 30 us,
-    // 35 in two)
-    while (items * p.splits < 1024 && p.splits * 16 < tiles) p.splits *= 2;
+    // Two or four waves to a workgroup while all fit the machine about at once (LDS and registers: 2048 waves of
+    // 16-bit rows of 128 dims, which also meet the memory's rate first; up to 4000 of the others).  512 rows of 16
+    // heads, 2048 keys, us, one wave and this: bf16 of 64 dims 38, 18, of 128 48, 35; E4M3 49, 23 and 60, 29;
+    // past the limits, 2046 rows of 768 keys: 25 and two waves 29; 38, 44
+    const int64_t most = fp8 ? 2560 : D == 64 ? 2048 : 1536;
+    while (p.waves < 4 && 4 * p.waves < tiles && 2 * items * p.waves <= most) p.waves *= 2;
   }
   const int64_t parts = (int64_t)p.waves * p.splits;
   p.per = ((tiles + parts - 1) / parts) * TILE;
