@@ -681,7 +681,8 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   // over workgroups, which a second kernel joins (4 us).  A 32-key step takes a lone wave about 1 us.
   p.waves = p.splits = 1;
   if (p.tiles == 1 && items <= 256) {
-    if (tiles > 32 && items < 128) {
+    // (of 128, those that share no cache rows: 16 rows x 8 cache heads, E4M3, 2048 keys: 25 us, 32 with eight waves)
+    if (tiles > 32 && (p.blocks == 1 ? items <= 128 : items < 128)) {
       // few rows, long lists: about one step to a wave.  1 row, 64 heads, 2048 keys: 9.9 us, 15.8 with eight
       // waves alone; 8 rows: 11.8 and 17.8
       p.waves = 4;
