@@ -372,8 +372,8 @@ idx_status idx_rope_freqs(int32_t rot, double base, int32_t scaling, double fact
                           double beta_fast, double beta_slow, double *freq, double *mscale);
 
 /* Rows of x rotated into out (same sizes and type).  out may be x itself, with the same
- * strides; otherwise the two share no byte.  D a multiple of 8, at most 512; T * H below 2^31 over the
- * power of two at or above D / 8 (that holds for every entry point with idx_rows but idx_sparse_attn). */
+ * strides; otherwise the two share no byte.  D a multiple of 8, at most 512; T * H times the power of two
+ * at or above D / 8 below 2^31, summed over the arrays of a call (idx_cache_write and _read likewise). */
 idx_status idx_rope(const idx_rows *x, const idx_rotary *r, const idx_rows *out, void *stream);
 
 /* A cache of `rows` slots with H rows of D values each; slot s, head h at s * ld + h * D elements.
@@ -406,8 +406,9 @@ typedef struct idx_write {
 } idx_write;
 
 /* Up to IDX_MAX_WRITES of them in one launch (a serving step's indexer query and key, attention key
- * and value).  The slots of one cache named in a call are distinct (IDX_DEBUG checks each array's):
- * a slot named twice holds bytes of either row.  The caches share no byte with the inputs. */
+ * and value).  The slots of one cache named in a call are distinct (IDX_DEBUG checks each array of up
+ * to 65536 rows): a slot named twice holds bytes of either row.  The caches share no byte with the
+ * inputs. */
 #define IDX_MAX_WRITES 8
 idx_status idx_cache_write(const idx_write *w, int32_t n, void *stream);
 

@@ -113,11 +113,14 @@ idx::RowJob row_job(const idx_rows &x, const idx_rotary *r, const int32_t *slot,
   return j;
 }
 
-// Rows that one launch does not reach: a lane to 8 values, fewer than 2^32 lanes.
-bool too_many(const idx_rows &x) {
+// A launch has a lane to 8 values, and fewer than 2^32 lanes.
+constexpr int64_t MAX_LANES = (int64_t)1 << 31;
+int64_t lanes_of(const idx_rows &x) {
+  const int64_t rows = (int64_t)x.T * x.H;
+  if (rows >= MAX_LANES) return MAX_LANES;
   int64_t lanes = 1;
   while (8 * lanes < x.D) lanes *= 2;
-  return (int64_t)x.T * x.H >= ((int64_t)1 << 31) / lanes;
+  return rows * lanes;
 }
 
 // The scale for powers of two.
@@ -210,7 +213,7 @@ idx_status idx_rope(const idx_rows *x, const idx_rotary *r, const idx_rows *out,
   if (x->dtype != out->dtype) return IDX_E_FORMAT;
   if (x->data == out->data && ((x->T > 1 && x->ld_t != out->ld_t) || (x->H > 1 && x->ld_h != out->ld_h)))
     return IDX_E_SHAPE;
-  if (too_many(*x)) return IDX_E_UNSUPPORTED;
+  if (lanes_of(*x) >= MAX_LANES) return IDX_E_UNSUPPORTED;
   const idx_cache to{out->data, nullptr, out->T, out->ld_t, 0, out->dtype, out->H, out->D};
   idx::RowJobs jobs{};
   jobs.job[0] = row_job(*x, r, nullptr, to);
@@ -223,6 +226,7 @@ idx_status idx_cache_write(const idx_write *w, int32_t n, void *stream) {
   if (n < 0 || n > IDX_MAX_WRITES) return IDX_E_PARAM;
   if (n > 0 && !w) return IDX_E_NULL;
   idx::RowJobs jobs{};
+  int64_t lanes = 0;
   for (int32_t i = 0; i < n; ++i) {
     idx_status st;
     if ((st = check_rows(w[i].x, false)) || (st = check_cache(w[i].to))) return st;
@@ -230,7 +234,8 @@ idx_status idx_cache_write(const idx_write *w, int32_t n, void *stream) {
     if (w[i].x.H != w[i].to.H || w[i].x.D != w[i].to.D) return IDX_E_SHAPE;
     if (!w[i].slot && w[i].x.T > w[i].to.rows) return IDX_E_SHAPE;
     if (!aligned(w[i].slot, 4)) return IDX_E_ALIGN;
-    if (too_many(w[i].x)) return IDX_E_UNSUPPORTED;
+    lanes += lanes_of(w[i].x);
+    if (lanes >= MAX_LANES) return IDX_E_UNSUPPORTED;
     jobs.job[i] = row_job(w[i].x, w[i].rotary, w[i].slot, w[i].to);
   }
   jobs.n = n;
@@ -247,7 +252,7 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
   if ((st = check_cache(*c)) || (st = check_rows(*out, true))) return st;
   if (c->H != out->H || c->D != out->D) return IDX_E_SHAPE;
   if (!aligned(rows, 4)) return IDX_E_ALIGN;
-  if (too_many(*out)) return IDX_E_UNSUPPORTED;
+  if (lanes_of(*out) >= MAX_LANES) return IDX_E_UNSUPPORTED;
   idx::ReadJob j{};
   j.data = (const uint8_t *)c->data;
   j.data_t = bytes_of(c->ld, c->fmt);

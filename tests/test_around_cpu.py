@@ -55,6 +55,8 @@ def test_rope_refusals(lib):
     assert rope(o=_rows(ld_t=2048)) == SHAPE
     many = dict(T=2 ** 24, H=8, ld_t=1024)                              # 2^27 rows of 16 lanes
     assert rope(x=_rows(**many), o=_rows(data=2 * F, **many)) == UNSUPPORTED
+    most = dict(T=2 ** 31 - 1, H=2 ** 28, ld_t=0, ld_h=0)               # rows that share memory
+    assert rope(x=_rows(**most), o=_rows(data=2 * F)) == SHAPE
     assert rope(x=_rows(T=0, data=None), o=_rows(T=0, data=None)) == OK
     assert rope(x=_rows(H=0, data=None), o=_rows(H=0, data=None)) == OK
 
@@ -79,6 +81,8 @@ def test_write_refusals(lib):
     assert write(r=_rotary(rot=136)) == SHAPE and write(r=_rotary(pos=None)) == NULL
     assert write(x=_rows(T=0, data=None)) == OK
     assert write(c=_cache(rows=0, data=None, scale=None)) == OK        # no slot to write
+    eight = (idx.idx_write * 8)(*[idx.idx_write(x=_rows(T=2 ** 21), slot=F, to=_cache()) for _ in range(8)])
+    assert lib.idx_cache_write(eight, 8, None) == UNSUPPORTED           # 2^31 lanes together
 
 
 def test_read_refusals(lib):
