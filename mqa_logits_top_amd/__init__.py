@@ -504,13 +504,16 @@ def _on(t: torch.Tensor, device, dtype, what: str) -> int:
 
 
 def _rows(x: torch.Tensor, what: str) -> idx_rows:
-    dtype = _VALUE.get(x.dtype)
-    if dtype is None or not x.is_cuda or x.dim() != 3 or (x.stride(2) != 1 and x.shape[2] > 1):
+    dtype, shape, ld = _VALUE.get(x.dtype), x.shape, x.stride()
+    if dtype is None or not x.is_cuda or len(shape) != 3 or (ld[2] != 1 and shape[2] > 1):
         raise ValueError(f"{what}: [T, H, D] bfloat16, float16 or float32 on the GPU with a contiguous last "
-                         f"dimension, got {list(x.shape)} {x.dtype} on {x.device}, strides {x.stride()}")
-    T, H, D = x.shape
-    ld_t, ld_h, _ = x.stride()
-    return idx_rows(x.data_ptr(), ld_t, ld_h, dtype, T, H, D)
+                         f"dimension, got {list(shape)} {x.dtype} on {x.device}, strides {ld}")
+    return idx_rows(x.data_ptr(), ld[0], ld[1], dtype, *shape)
+
+
+def _new_rows(x: torch.Tensor, dtype: int, T: int, H: int, D: int) -> idx_rows:
+    """Of a tensor just allocated with these sizes."""
+    return idx_rows(x.data_ptr(), H * D, D, dtype, T, H, D)
 
 
 class _on_stream:
@@ -659,9 +662,12 @@ def idx_rope(x: torch.Tensor, pos: torch.Tensor, rotary: Rotary, out: Optional[t
     with _on_stream(device, stream) as st:
         if out is None:
             out = x.new_empty(x.shape)
+            to = _new_rows(out, rows.dtype, *x.shape)
         elif out.device != device:
             raise ValueError(f"out on {out.device} for x on {device}")
-        s = load_library().idx_rope(rows, r, _rows(out, "out"), st)
+        else:
+            to = _rows(out, "out")
+        s = load_library().idx_rope(rows, r, to, st)
     if s:
         raise IdxError("idx_rope", s)
     return out
@@ -706,10 +712,15 @@ def idx_cache_read(cache: Cache, rows: Optional[torch.Tensor] = None, out: Optio
         at, n = _on(rows, device, torch.int32, "rows"), rows.shape[0]
     with _on_stream(device, stream) as st:
         if out is None:
+            if dtype not in _VALUE:
+                raise ValueError(f"dtype: bfloat16, float16 or float32, got {dtype}")
             out = cache._data.new_empty((n, cache.H, cache.D), dtype=dtype)
+            to = _new_rows(out, _VALUE[dtype], n, cache.H, cache.D)
         elif out.device != device or out.shape[0] != n:
             raise ValueError(f"out: {n} rows on {device}")
-        s = load_library().idx_cache_read(cache._struct, at, _rows(out, "out"), st)
+        else:
+            to = _rows(out, "out")
+        s = load_library().idx_cache_read(cache._struct, at, to, st)
     if s:
         raise IdxError("idx_cache_read", s)
     return out
@@ -743,14 +754,17 @@ def idx_sparse_attn(q: torch.Tensor, k: Cache, v: Cache, sel: torch.Tensor, scal
     with _on_stream(device, stream) as st:
         if out is None:
             out = q.new_empty(q.shape)
+            to = _new_rows(out, rows.dtype, *q.shape)
         elif out.device != device:
             raise ValueError(f"out on {out.device} for q on {device}")
+        else:
+            to = _rows(out, "out")
         if lse is None:
             if with_lse:
                 lse = q.new_empty((T, Hq), dtype=torch.float32)
         elif lse.shape != (T, Hq):
             raise ValueError(f"lse: {[T, Hq]}")
-        a = idx_attn(rows, _rows(out, "out"), k._struct, v._struct, sel.data_ptr(), sel.stride(0), sel.shape[1], pool,
+        a = idx_attn(rows, to, k._struct, v._struct, sel.data_ptr(), sel.stride(0), sel.shape[1], pool,
                      a_ks, a_ke, table, L, scale, None if lse is None else _on(lse, device, torch.float32, "lse"))
         at, size = None, 0
         if ws is None:
