@@ -16,15 +16,11 @@ FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
     # packed fp32 VALU ops are kept out of every kernel
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    # MFMA results go straight to VGPRs: the scoring epilogue reads every
+    # accumulator once, so AGPR destinations would cost one v_accvgpr_read each
+    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall", "-Wno-unused-function",
 ]
-# MFMA results go straight to VGPRs: the scoring epilogue reads every
-# accumulator once, so AGPR destinations would cost one v_accvgpr_read each
-MFMA_VGPR = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-# The attention kernel keeps its output accumulators for the whole row and reads them when a
-# maximum grows: they stay in AGPRs, which leaves the VGPRs to the operands (64 heads of 128 dims
-# take 128 accumulators and 64 registers of queries; VGPRs alone would spill)
-AGPR_SOURCES = ("attn.hip",)
 
 
 def sources():
@@ -47,8 +43,7 @@ def build(verbose: bool = False) -> str:
     try:
         def compile_one(src):
             obj = os.path.join(work, os.path.basename(src) + ".o")
-            flags = FLAGS + ([] if os.path.basename(src) in AGPR_SOURCES else MFMA_VGPR)
-            return obj, _run(["hipcc", *flags, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj])
+            return obj, _run(["hipcc", *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj])
 
         with ThreadPoolExecutor(JOBS) as pool:
             done = list(pool.map(compile_one, sources()))
