@@ -336,3 +336,53 @@ def test_binding_refusals():
         idx.idx_cache_write([idx.Write(x[:, :1], c)])
     with pytest.raises(AttributeError):
         c.data = x
+
+
+@pytest.mark.parametrize("fmt", [FP8, FP4, idx.IDX_K_BF16, idx.IDX_K_F32])
+def test_nothing_to_do(fmt):
+    """No rows, a cache without slots, an empty list: nothing is written, reads outside are zeros."""
+    plan = idx.Rotary.make(32)
+    none, pos = _x(1, 0, 3, 64).cuda(), torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert idx.idx_rope(none, pos, plan).shape == (0, 3, 64)
+    c, empty = idx.Cache.empty(4, 3, 64, fmt), idx.Cache.empty(0, 3, 64, fmt)
+    before = c.data.clone()
+    idx.idx_cache_write([])
+    idx.idx_cache_write([idx.Write(none, c, rotary=plan, pos=pos), idx.Write(none, empty)])
+    far = torch.tensor([0, 5, -1, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device="cuda")
+    idx.idx_cache_write([idx.Write(_x(2, 5, 3, 64).cuda(), empty, slot=far)])
+    assert torch.equal(c.data, before)
+    assert idx.idx_cache_read(c, pos).shape == (0, 3, 64) and idx.idx_cache_read(empty).shape == (0, 3, 64)
+    assert not idx.idx_cache_read(empty, far).any()
+
+
+def test_graph_and_streams():
+    """Captured calls take what their inputs hold at each replay; calls on another stream give the same."""
+    plan = idx.Rotary.make(64, layout=1)
+    x, pos = _x(3, 9, 4, 128).cuda(), torch.arange(9, dtype=torch.int32, device="cuda")
+    slot = torch.arange(9, dtype=torch.int32, device="cuda") * 2
+    caches = [idx.Cache.empty(40, 4, 128, f) for f in (FP8, FP4, idx.IDX_K_BF16)]
+
+    def run(stream=None):
+        y = idx.idx_rope(x, pos, plan, stream=stream)
+        idx.idx_cache_write([idx.Write(x, c, slot=slot, rotary=plan, pos=pos) for c in caches], stream=stream)
+        return [y] + [idx.idx_cache_read(c, slot, stream=stream) for c in caches]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for turn in range(4):
+        x.copy_(_x(10 + turn, 9, 4, 128))
+        pos.add_(1000)
+        slot.add_(1)
+        want = [y.clone() for y in run()]
+        for c in caches:
+            c.data.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))
+        side = torch.cuda.Stream()
+        got = run(side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))

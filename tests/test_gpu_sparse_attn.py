@@ -33,6 +33,11 @@ def _check(q, k, v, sel, scale, pool=1, ks=None, ke=None, table=None, **kw):
     cu = lambda a: None if a is None else torch.as_tensor(a, dtype=torch.int32).cuda()
     out, lse = idx.idx_sparse_attn(q.cuda(), k, v, cu(sel), scale, pool=pool, ks=cu(ks), ke=cu(ke),
                                    slot_of_key=cu(table), **kw)
+    _compare(out, lse, q, k, v, sel, scale, pool, ks, ke, table)
+    return out, lse
+
+
+def _compare(out, lse, q, k, v, sel, scale, pool=1, ks=None, ke=None, table=None):
     rows = keys_of(np.asarray(sel), ks, ke, pool, k.rows if table is None else len(table), table, k.rows)
     # fp16 with E4M3 caches: weights in two bf16 parts, the second's half step of what the first left
     step = 2.0 ** -8 if q.dtype == torch.bfloat16 else 2.0 ** -16 if k.fmt == FP8 else 2.0 ** -11
@@ -43,7 +48,6 @@ def _check(q, k, v, sel, scale, pool=1, ks=None, ke=None, table=None, **kw):
     assert (err <= bo).all(), f"out: {(err > bo).sum()} off, worst {np.max(err / bo):.2f} of the bound"
     fin = np.isfinite(wl)
     assert (np.abs(gl[fin] - wl[fin]) <= bl[fin]).all(), "lse"
-    return out, lse
 
 
 def _sel(rng, T, n, L, holes=0.0):
@@ -93,7 +97,8 @@ def test_many_rows_of_many_heads(dtype, fp8, D, T, Hq, n):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("T,Hkv,n", [(300, 1, 700), (33, 8, 900), (2, 2, 3000), (130, 1, 300)])
+@pytest.mark.parametrize("T,Hkv,n", [(300, 1, 700), (33, 8, 900), (2, 2, 3000), (130, 1, 300),
+                                     (900, 1, 200), (128, 1, 1100), (16, 8, 1100)])
 def test_divided_lists(T, Hkv, n, fp8):
     """Lists divided over workgroups, over waves, and over both; holes and an empty row among them."""
     rng = np.random.default_rng(n)
@@ -339,6 +344,65 @@ def test_two_graphs_beside_each_other():
         torch.cuda.synchronize()
         for g, out, want, _, _ in calls:
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_cache_of_many_heads(fp8):
+    """Rows of a cache that no on-chip memory holds are divided over workgroups of one wave."""
+    rng = np.random.default_rng(12)
+    H, rows = 8, 140_000 if fp8 else 70_000                                     # 143 MB both
+    k, v = _caches(41, rows, H, 64, torch.bfloat16, fp8)
+    q, s = _q(42, 40, 4 * H, 64, torch.bfloat16), _sel(rng, 40, 2 * rows // 40, rows)
+    take = slice(17, 20)                                                        # three rows against 64 bits
+    out, lse = idx.idx_sparse_attn(q.cuda(), k, v, torch.from_numpy(s).cuda(), 0.12)
+    at = [np.unique(s[take]), None]
+    at[1] = np.searchsorted(at[0], s[take]).astype(np.int32)
+    few = torch.from_numpy(at[0]).long().cuda()
+    small = [idx.Cache(c.data[few], None if c.scale is None else c.scale[few], fmt=c.fmt) for c in (k, v)]
+    _compare(out[take], lse[take], q[take], *small, at[1], 0.12)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nothing_to_attend_to(fp8):
+    """No rows, no entries, no keys, a cache without slots."""
+    k, v = _caches(1, 20, 2, 64, torch.bfloat16, fp8)
+    e = [idx.Cache.empty(0, 2, 64, k.fmt) for _ in range(2)]
+    q = _q(1, 3, 4, 64, torch.bfloat16).cuda()
+    ids = lambda *shape: torch.zeros(shape, dtype=torch.int32, device="cuda")
+    out, lse = idx.idx_sparse_attn(q[:0], k, v, ids(0, 5), 0.1)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    for c, s, kw in ((k, v), ids(3, 0), {}), (e, ids(3, 5), {}), (e, ids(3, 2000), {}), ((k, v), ids(3, 5), dict(
+            slot_of_key=ids(0))), ((k, v), ids(3, 5), dict(ks=ids(3), ke=ids(3))), (e, ids(3, 5), dict(
+            slot_of_key=ids(9))):
+        out, lse = idx.idx_sparse_attn(q, *c, s, 0.1, **kw)
+        assert not out.any() and torch.isneginf(lse).all()
+
+
+def test_two_threads():
+    """Two host threads, each with its stream."""
+    import threading
+    rng = np.random.default_rng(13)
+    k, v = _caches(43, 3000, 1, 128, torch.bfloat16, True)
+    q = [_q(44 + i, 3, 32, 128, torch.bfloat16).cuda() for i in range(2)]
+    s = [torch.from_numpy(_sel(rng, 3, 1500, 3000)).cuda() for _ in range(2)]
+    want = [idx.idx_sparse_attn(q[i], k, v, s[i], 0.1) for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        side = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(idx.idx_sparse_attn(q[i], k, v, s[i], 0.1, stream=side))
+        side.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        assert all(torch.equal(o, want[i][0]) and torch.equal(l, want[i][1]) for o, l in got[i])
 
 
 def test_repeatable_and_other_streams():
