@@ -681,8 +681,10 @@ hipError_t launch_dim(const AttnArgs &a, int D, int tiles, unsigned blocks, hipS
 AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64_t entries, int64_t touched) {
   AttnPlan p{};
   const int64_t tiles = entries > 0 ? (entries + TILE - 1) / TILE : 1;
-  // 32 heads to a wave where rows alone fill the machine (2 waves a SIMD): each key is fetched once for them
-  p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 1024 ? 2 : 1;
+  // 32 heads to a wave where rows alone nearly fill the machine (2 waves a SIMD): each key is fetched once for them.
+  // 32 heads of 128, 2048 keys, us, with 16 heads a wave and with 32: 2048 rows 196, 112 in bf16 and 172, 112 in E4M3;
+  // 768 rows 85, 61 and 83, 68; 512 rows 60, 60 and 58, 70
+  p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 768 ? 2 : 1;
   const int32_t heads = 16 * p.tiles;
   p.blocks = (G + heads - 1) / heads;
   const int64_t items = (int64_t)T * Hkv * p.blocks;
@@ -690,15 +692,14 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   // over workgroups, which a second kernel joins (4 us).  A 32-key step takes a lone wave about 1 us.
   p.waves = p.splits = 1;
   if (p.tiles == 1 && items <= 256) {
-    // (of 128, those that share no cache rows: 16 rows x 8 cache heads, E4M3, 2048 keys: 25 us, 32 with eight waves)
     if (tiles > 32 && (p.blocks == 1 ? items <= 128 : items < 128)) {
       // few rows, long lists: about one step to a wave.  1 row, 64 heads, 2048 keys: 9.9 us, 15.8 with eight
-      // waves alone; 8 rows: 11.8 and 17.8
+      // waves alone; 8 rows: 11.8 and 17.8; 128 that share no cache rows (16 rows x 8 cache heads, E4M3): 25 and 32
       p.waves = 4;
       while (items * p.waves * p.splits < 1024 && p.waves * p.splits < tiles && p.splits < MAX_SPLITS) p.splits *= 2;
     } else {
-      // 32 rows, 64 heads, 2048 keys: 17.3 us, 21.2 with four waves and two workgroups; 256 rows, 16 heads, 512
-      // keys: 15.9 us, 17.3 with one wave
+      // 32 rows, 64 heads (128 that share rows), 2048 keys: 17.3 us, 21.2 with four waves and two workgroups; 256
+      // rows, 16 heads, 512 keys: 15.9 us, 17.3 with one wave
       while (p.waves < MAX_WAVES && p.waves < tiles && items * p.waves < 1024) p.waves *= 2;
     }
   } else if (p.tiles == 1 && items <= 384 && tiles > 32 && touched > FROM_MEMORY) {

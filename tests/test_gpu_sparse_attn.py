@@ -84,7 +84,7 @@ def test_list_lengths(T, n, fp8):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("T,Hq,n", [(1030, 32, 70), (600, 50, 33), (512, 64, 100)])
+@pytest.mark.parametrize("T,Hq,n", [(1030, 32, 70), (600, 50, 33), (512, 64, 100), (385, 40, 65)])
 def test_many_rows_of_many_heads(dtype, fp8, D, T, Hq, n):
     """Rows that fill the machine take 32 heads to a wave."""
     rng = np.random.default_rng(T)
