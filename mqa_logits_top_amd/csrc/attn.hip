@@ -10,7 +10,10 @@
 // The softmax is the running one: a reference near the maximum, the sum, the unnormalised output.  The weights
 // of the second product are rounded to 16 bits; the output is divided by the sum of the rounded ones (a product
 // with ones), so that a row whose weight lies on few keys gains little error from it.  E4M3 caches put a key's
-// scale into its weight, whose rounding has no such sum: there weights are two 16-bit parts (TWO).
+// scale into its weight, whose rounding has no such sum (one key's value would come out rounded twice): there weights
+// are two parts of 8 bits, in every variant, so that a row's precision is the same whatever rows are beside it.  The
+// second part takes 18% of the time of 32 heads a wave (2048 rows x 512 keys, 64 heads: 61 us without it), none of 16
+// heads a wave (40 rows x 8 cache heads: 49.8 us, 49.6).
 // Cache rows reach LDS by memory-to-LDS copies that each bring whole rows, K for the next step while this one
 // multiplies, V while the next one's scores are computed.  Waves of the 2000 rows that are resident at once
 // walk their ascending lists at the same pace, so each XCD's L2 meets a row's neighbours' keys soon after.
@@ -19,8 +22,8 @@
 // however few they are in memory.  D = 128, 2 waves a SIMD by registers.
 //   2048 rows x 2048 of 65536 keys, 32 heads on one bf16 cache head: 100 us, 690 TFLOP/s (58 us at the rate of a
 //     large product); 2.1 GB through the L2s at 21 TB/s, which reach 27 with nothing but such loads (80 us).
-//   2048 rows x 512 of 102400, 64 heads, E4M3: 60 us, 560 TFLOP/s (29 us): vector instructions, a third of them
-//     conversions of codes, and matrix instructions issue for 50% and 22% of the time.
+//   2048 rows x 512 of 102400, 64 heads, E4M3: 73 us, 470 TFLOP/s (29 us): vector instructions, conversions of codes
+//     and of weights first among them, and matrix instructions, half as many again for the weights' second part.
 //   40 rows x 2048 of 4000 each, 32 heads on 8, E4M3, paged: 48 us, 3.6 TB/s (36 us): scattered 1 KB slots.
 //   1023 rows x 96 blocks of 8 keys, 16 heads of 64 on 2, fp16: 22 us: 0.4 GB gathered at 18 TB/s.
 //   1 row x 512 keys, 64 heads, bf16: 8.4 us, of which 3.6 are a launch and the rest three loads' latencies in turn
@@ -156,11 +159,7 @@ constexpr int waves_a_simd(bool fp8, int D, int mt) { return (D == 64 ? 3 : 2) +
 // MT = 1 may run several waves a workgroup, which divide the entries and join through LDS.
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D, MT)) void attn_kernel(AttnArgs a) {
-  constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range ...
-  // ... and two parts of 8 bits: an fp16 result needs them, and a wave of 16 heads has the time (40 rows x 8 cache
-  // heads: 52.8 us, 52.6 with one part).  With 32 heads a bf16 result has one part: 62 us, 73 with two (2048 rows x
-  // 64 heads x 512 keys); it errs by 1.4 of its own rounding.
-  constexpr bool TWO = FP8 && (!BF16 || MT == 1);
+  constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range, and two parts for precision
   constexpr uint32_t ONES = BF16 ? 0x3F803F80u : 0x3C003C00u;
   constexpr int KS = D / 32;              // steps of the first product
   constexpr int DN = D / 16;              // tiles of the second product
@@ -450,7 +449,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D,
           y *= vsc[2 * i + 1];
         }
         p[m][i] = pack2<PV_BF16>(x, y);
-        if constexpr (TWO)
+        if constexpr (FP8)
           rest[m][i] = pack2<PV_BF16>(x - __uint_as_float(p[m][i] << 16), y - __uint_as_float(p[m][i] & 0xFFFF0000u));
       }
     }
@@ -508,7 +507,7 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D,
 #pragma unroll
       for (int d = 0; d < DN; ++d) {
         o[m][d] = mfma<PV_BF16>(vt[d], p[m], o[m][d]);
-        if constexpr (TWO) o[m][d] = mfma<PV_BF16>(vt[d], rest[m], o[m][d]);
+        if constexpr (FP8) o[m][d] = mfma<PV_BF16>(vt[d], rest[m], o[m][d]);
       }
     }
   }
@@ -682,8 +681,10 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   AttnPlan p{};
   const int64_t tiles = entries > 0 ? (entries + TILE - 1) / TILE : 1;
   // 32 heads to a wave where rows alone nearly fill the machine (2 waves a SIMD): each key is fetched once for them.
-  // 32 heads of 128, 2048 keys, us, with 16 heads a wave and with 32: 2048 rows 196, 112 in bf16 and 172, 112 in E4M3;
-  // 768 rows 85, 61 and 83, 68; 512 rows 60, 60 and 58, 70
+  // From 768 waves on 32 heads are as fast or faster with 24, 32 and 64 query heads, 64 and 128 dims, 512 and 2048 keys,
+  // either type of cache.  us with 16 heads a wave and with 32, 2048 keys, 32 heads of 128 and of 64: E4M3, 512 rows
+  // 53, 82 and 41, 63; 768 rows 81, 83 and 64, 63; 1024 rows 90, 83 and 67, 63; 2048 rows 160, 123 and 127, 90; bf16,
+  // 512 rows 53, 58 and 31, 47; 768 rows 75, 57 and 46, 47; 1024 rows 90, 60 and 52, 49; 2048 rows 171, 99 and 97, 65
   p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 768 ? 2 : 1;
   const int32_t heads = 16 * p.tiles;
   p.blocks = (G + heads - 1) / heads;
