@@ -160,6 +160,11 @@ constexpr int waves_a_simd(bool fp8, int D, int mt) { return (D == 64 ? 3 : 2) +
 template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D, MT)) void attn_kernel(AttnArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range, and two parts for precision
+  // Weights are exp2(score - reference), below 2^8 with the reference where it was when last moved.  In fp16 they lie
+  // 2^7 higher, below 2^15 (of 2^16): those under its smallest normal number, which lose up to 2^-25 whatever their size,
+  // are then 2^-21 of the largest and less instead of 2^-14, and long lists of small weights keep their sum.  No time:
+  // 1023 rows of 8-key blocks 23.6 us, 23.3 without it.
+  constexpr float LIFT = !PV_BF16 ? 7.f : 0.f;
   constexpr uint32_t ONES = BF16 ? 0x3F803F80u : 0x3C003C00u;
   constexpr int KS = D / 32;              // steps of the first product
   constexpr int DN = D / 16;              // tiles of the second product
@@ -426,11 +431,11 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D,
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const float top = max8(sc[m]) * a.scale2;   // scale2 > 0: the largest product is the largest dot's
-      // The reference moves only when a score is 2^8 above it: weights then stay below 2^8, and the
+      // The reference (LIFT below the largest score) moves only when a score is 2^8 above that: the
       // accumulators are rescaled a few times a row instead of at most tiles.  The four lanes of a head
       // share their reference, so a lane's own scores decide whether there is anything to do.
-      if (__any(top > ref[m] + 8.f)) {
-        const float to = __builtin_fmaxf(ref[m], head_max(top));
+      if (__any(top > ref[m] + (8.f + LIFT))) {
+        const float to = __builtin_fmaxf(ref[m], head_max(top) - LIFT);
         const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
         sum[m] *= f;
         rounded[m] *= f;

@@ -33,3 +33,38 @@ def test_e4m3_weights_in_two_parts(dtype, T, Hq, D, n):
     want, _, bound, _ = attend(q.double().numpy(), kd, vd, list(sel.astype(np.int64)), 0.1, 2.0 ** -16, dtype)
     err = np.abs(out.cpu().double().numpy() - want)
     assert (err <= bound).all(), f"{(err > bound).sum()} off, worst {np.max(err / bound):.2f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("T,Hq,D,n", [(1, 8, 64, 40000), (150, 16, 64, 20000), (800, 32, 64, 20000),
+                                      (800, 32, 128, 20000), (400, 8, 128, 20000)])
+def test_many_small_weights(dtype, first, T, Hq, D, n):
+    """One key of score 0 and value 0, and n whose weight is exp(-17.75), 2^-25.6 of it, with values of 1/2 to 3/2:
+    together they are the output.  A weight is rounded relatively, and by at most 2^-32 of the largest beside."""
+    rng = np.random.default_rng(n)
+    data = [torch.zeros((n + 1, 1, D), dtype=dtype) for _ in range(2)]
+    at = 0 if first else n
+    data[0][:, 0, 0] = -17.75
+    data[0][at, 0, 0] = 0.0
+    data[1][:] = torch.from_numpy(rng.uniform(0.5, 1.5, (n + 1, 1, D))).to(dtype)
+    data[1][at] = 0.0
+    fmt = idx.IDX_K_F16 if dtype == torch.float16 else idx.IDX_K_BF16
+    k, v = (idx.Cache(x.cuda(), fmt=fmt) for x in data)
+    q = torch.zeros((T, Hq, D), dtype=dtype)
+    q[:, :, 0] = 1.0
+    sel = torch.arange(n + 1, dtype=torch.int32, device="cuda").expand(T, n + 1).contiguous()
+    out, lse = idx.idx_sparse_attn(q.cuda(), k, v, sel, 1.0)
+    w = np.exp(np.where(np.arange(n + 1) == at, 0.0, -17.75))
+    x = data[1][:, 0].double().numpy()
+    want = (w @ x / w.sum())[None, None]
+    # each weight rounded by `step` relative, and by 2^-32 of the largest in fp16, in numerator and divisor (whose
+    # change by them is below 2^-15 relative); sums of n terms in fp32; the score (in units of ln 2, once rounded) and
+    # the exponential 2^-19; the result's rounding, where fp16 has steps of 2^-24 at least
+    step, half = (2.0 ** -11, 2.0 ** -11) if dtype == torch.float16 else (2.0 ** -8, 2.0 ** -8)
+    bound = (step + 2.0 ** -15 + 2.0 ** -19 + n * 2.0 ** -23 + half) * want + 2.0 ** -25
+    if dtype == torch.float16:
+        bound = bound + 2.0 ** -32 * x.sum(0)
+    err = np.abs(out.cpu().double().numpy() - want)
+    assert (err <= bound).all(), f"{(err > bound).sum()} off, worst {np.max(err / bound):.2f} of the bound"
+    assert np.abs(lse.cpu().double().numpy() - np.log(w.sum())).max() <= 2.0 ** -19 + n * 2.0 ** -23
