@@ -10,6 +10,7 @@ Function names match the C entry points.  Tensors must be on the GPU and
 contiguous; key indices in outputs are absolute rows of k.  The operators around
 the indexer (idx_rope, idx_cache_write, idx_cache_read, idx_sparse_attn) check
 types, shapes and devices here, and take any strides the C entry points take.
+They record no gradient and refuse rows that require one while autograd is on.
 """
 from __future__ import annotations
 
@@ -504,6 +505,9 @@ def _on(t: torch.Tensor, device, dtype, what: str) -> int:
 
 
 def _rows(x: torch.Tensor, what: str) -> idx_rows:
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires a gradient, and no entry point records one: call it under torch.no_grad() "
+                         "or on x.detach() (idx_rope's gradient is idx_rope with inverse=True)")
     dtype, shape, ld = _VALUE.get(x.dtype), x.shape, x.stride()
     if dtype is None or not x.is_cuda or len(shape) != 3 or (ld[2] != 1 and shape[2] > 1):
         raise ValueError(f"{what}: [T, H, D] bfloat16, float16 or float32 on the GPU with a contiguous last "

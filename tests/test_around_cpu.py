@@ -177,3 +177,16 @@ def test_binding_refuses_tensors_off_the_gpu():
     assert idx.idx_cache_write([]) is None
     with pytest.raises(idx.IdxError):
         idx.idx_rope_freqs(63)
+
+
+def test_binding_refuses_rows_that_require_a_gradient():
+    """No entry point records a gradient: a call that would drop one without a word is an error, unless autograd
+    is off."""
+    x = torch.zeros((2, 4, 128), dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="requires a gradient"):
+        idx._rows(x, "x")
+    with pytest.raises(ValueError, match="requires a gradient"):
+        idx._rows(x * 2, "x")
+    for quiet in (torch.no_grad, torch.inference_mode):
+        with quiet(), pytest.raises(ValueError, match="on the GPU"):
+            idx._rows(x, "x")
