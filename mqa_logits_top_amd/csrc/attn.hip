@@ -161,9 +161,9 @@ template <bool BF16, bool FP8, int D, int MT, bool WIDE>
 __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D, MT)) void attn_kernel(AttnArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range, and two parts for precision
   // Weights are exp2(score - reference), below 2^8 with the reference where it was when last moved.  In fp16 they lie
-  // 2^7 higher, below 2^15 (of 2^16): those under its smallest normal number, which lose up to 2^-25 whatever their size,
-  // are then 2^-21 of the largest and less instead of 2^-14, and long lists of small weights keep their sum.  No time:
-  // 1023 rows of 8-key blocks 23.6 us, 23.3 without it.
+  // 2^7 higher, below 2^15 (of 2^16): those under its smallest normal number, which lose up to 2^-25 whatever their
+  // size, are then 2^-21 of the largest and less instead of 2^-14, and long lists of small weights keep their sum.
+  // No time: 1023 rows of 8-key blocks 23.6 us, 23.3 without it.
   constexpr float LIFT = !PV_BF16 ? 7.f : 0.f;
   constexpr uint32_t ONES = BF16 ? 0x3F803F80u : 0x3C003C00u;
   constexpr int KS = D / 32;              // steps of the first product
@@ -686,9 +686,9 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   AttnPlan p{};
   const int64_t tiles = entries > 0 ? (entries + TILE - 1) / TILE : 1;
   // 32 heads to a wave where rows alone nearly fill the machine (2 waves a SIMD): each key is fetched once for them.
-  // From 768 waves on 32 heads are as fast or faster with 24, 32 and 64 query heads, 64 and 128 dims, 512 and 2048 keys,
-  // either type of cache.  us with 16 heads a wave and with 32, 2048 keys, 32 heads of 128 and of 64: E4M3, 512 rows
-  // 53, 82 and 41, 63; 768 rows 81, 83 and 64, 63; 1024 rows 90, 83 and 67, 63; 2048 rows 160, 123 and 127, 90; bf16,
+  // From 768 waves on 32 heads are as fast or faster with 24, 32 and 64 query heads, 64 and 128 dims, 512 and 2048
+  // keys, either type of cache.  us with 16 heads a wave and with 32, 2048 keys, 32 heads of 128 and of 64: E4M3,
+  // 512 rows 53, 82 and 41, 63; 768 rows 81, 83 and 64, 63; 1024 rows 90, 83 and 67, 63; 2048 rows 160, 123 and 127, 90; bf16,
   // 512 rows 53, 58 and 31, 47; 768 rows 75, 57 and 46, 47; 1024 rows 90, 60 and 52, 49; 2048 rows 171, 99 and 97, 65
   p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 768 ? 2 : 1;
   const int32_t heads = 16 * p.tiles;
@@ -698,20 +698,29 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   // over workgroups, which a second kernel joins (4 us).  A 32-key step takes a lone wave about 1 us.
   p.waves = p.splits = 1;
   if (p.tiles == 1 && items <= 256) {
-    if (tiles > 32 && (p.blocks == 1 ? items <= 128 : items < 128)) {
+    if (tiles > 32 && items <= 128) {
       // few rows, long lists: about one step to a wave.  1 row, 64 heads, 2048 keys: 9.9 us, 15.8 with eight
-      // waves alone; 8 rows: 11.8 and 17.8; 128 that share no cache rows (16 rows x 8 cache heads, E4M3): 25 and 32
+      // waves alone; 8 rows: 11.8 and 17.8.  Up to half the CUs: 128 items, us with four waves and two workgroups and
+      // with eight waves alone, E4M3 and bf16: 16 rows x 8 cache heads 24, 29 and 33, 38; 128 rows of 16 heads, cache
+      // rows of their own 24, 23 and 34, 33, shared 18, 17 and 17, 18; 32 rows of 64 heads 18, 16 and 18, 18
       p.waves = 4;
       while (items * p.waves * p.splits < 1024 && p.waves * p.splits < tiles && p.splits < MAX_SPLITS) p.splits *= 2;
     } else {
-      // 32 rows, 64 heads (128 that share rows), 2048 keys: 17.3 us, 21.2 with four waves and two workgroups; 256
-      // rows, 16 heads, 512 keys: 15.9 us, 17.3 with one wave
+      // One workgroup for 129 to 256 items: of 20 divisions up to 8 waves and 16 workgroups the best one, or within 5%
+      // of it, for 16 and 64 heads on one cache head and from 24 rows x 8 on (200 rows of 16 heads, E4M3: 33 us, 43
+      // with eight workgroups of a wave; 24 rows x 8: 35.5, 34.5); 17 to 20 rows x 8 in E4M3 lose 14% (31.6, 27.1).
+      // 256 rows, 16 heads, 512 keys: 15.9 us, 17.3 with one wave
       while (p.waves < MAX_WAVES && p.waves < tiles && items * p.waves < 1024) p.waves *= 2;
     }
-  } else if (p.tiles == 1 && items <= 384 && tiles > 32 && touched > FROM_MEMORY) {
-    // Rows that come from memory are read at its rate only if every CU asks for its share, which 320 workgroups of
-    // four waves on 256 CUs do not: 40 rows x 8 cache heads of a 330 MB cache, 2048 keys: 53 us, 63 that way
-    while (items * p.splits < 1024) p.splits *= 2;
+  } else if (p.tiles == 1 && items <= 384 && tiles > 32 && Hkv > 1 && touched > FROM_MEMORY) {
+    // More items than CUs, and up to one and a half: a workgroup each leaves some CUs twice the others' share of what
+    // memory brings, and the heads of a slot, which lie together, are read apart.  2048 keys of 128 dims through a slot
+    // table, us, four workgroups of a wave and one of four, E4M3 and bf16: 33 rows x 8 cache heads 47, 53 and 68, 76;
+    // 40 rows 51, 63 and 75, 80; 48 rows 59, 65 and 87, 85; 96 rows x 4 58, 60 and 89, 86; 180 rows x 2 56, 57 and 81,
+    // 80 (slots in order: 51, 47 and 81, 78).  Past it a workgroup each is as fast or faster (52 rows x 8 66, 67 and 95,
+    // 88), and so it is for one cache head (400 rows of 16 heads 78, 66 and 95, 84), rows that a cache on the chip holds
+    // (300 of 16 heads 35, 26) and shorter lists (33 rows x 8, 512 keys: 17.5, 15.5)
+    p.splits = 4;
   } else if (p.tiles == 1) {
     // Two or four waves to a workgroup while all fit the machine about at once (LDS and registers: 2048 waves of
     // 16-bit rows of 128 dims, which also meet the memory's rate first; up to 4000 of the others).  512 rows of 16

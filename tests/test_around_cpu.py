@@ -190,3 +190,31 @@ def test_binding_refuses_rows_that_require_a_gradient():
     for quiet in (torch.no_grad, torch.inference_mode):
         with quiet(), pytest.raises(ValueError, match="on the GPU"):
             idx._rows(x, "x")
+
+
+def _workgroups_of_a_row(lib, T, H, G, n=2048, L=4000, fmt=FP8, D=128):
+    """Workgroups that a row's list is divided over, from the workspace that joins them (1: no workspace), for rows of
+    16 heads a wave on caches of `T` requests."""
+    bytes_ = ctypes.c_size_t()
+    cache = _cache(rows=T * L, H=H, D=D, fmt=fmt)
+    a = _attn(q=_rows(T=T, H=H * G, D=D), out=_rows(T=T, H=H * G, D=D, data=2 * F), k=cache, v=cache, n_sel=n, ld_sel=n,
+              L=T * L)
+    assert lib.idx_sparse_attn_workspace(a, bytes_) == OK
+    part = T * H * -(-G // 16) * 16 * (D + 4) * 4
+    assert bytes_.value % part == 0
+    return max(bytes_.value // part, 1)
+
+
+def test_lists_are_divided_by_the_work_there_is(lib):
+    """How a list is divided goes by the items (rows x cache heads x blocks of 16 heads), not by which of the three they
+    come from, and changes at few sizes."""
+    of = lambda *a, **kw: _workgroups_of_a_row(lib, *a, **kw)
+    assert of(128, 1, 16) == of(16, 8, 4) == of(32, 1, 64) == of(64, 1, 32) == 2
+    assert of(64, 1, 16) == of(8, 8, 4) == of(16, 1, 64) == 4
+    for H in (4, 8, 16):                 # past the number of CUs, from memory
+        assert {of(T, H, 4) for T in range(272 // H, 384 // H + 1)} == {4}, H
+        assert {of(T, H, 4, n=512) for T in range(272 // H, 384 // H + 1)} == {1}, H
+        assert {of(T, H, 4) for T in range(144 // H, 256 // H + 1)} == {1}, H
+    assert {of(T, 1, 16) for T in range(129, 500)} == {1}
+    counts = [of(T, 8, 4) for T in range(1, 97)]
+    assert sum(a != b for a, b in zip(counts[15:], counts[16:])) == 3   # 2, 1, 4, 1
