@@ -428,7 +428,10 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
  * A key's cache row is the key itself, or slot_of_key[key] where that table (int32 [L]) is given; a
  * row outside the caches does not count.  Every entry is a term of its own: an id listed twice counts
  * twice.  Rows that do not count are not read, so what they hold reaches no output.  The order of
- * entries has no influence beyond the rounding of sums; results are bitwise repeatable.
+ * entries has no influence beyond the rounding of sums.  A call's results are bitwise repeatable, and a
+ * row's do not depend on what the other rows hold.  Its bits do depend on the call's sizes (T, heads,
+ * n_sel * pool, slots), by which its list is divided and its sums are rounded in another order: the same
+ * row in a chunk of another length agrees within the bounds below, not bit for bit.
  * q and out share type and sizes, IDX_K_BF16 or IDX_K_F16; the caches are of that type or E4M3, both
  * alike, with the same slots and strides; D = 64 or 128; T * Hq below 2^26.  Products run on the matrix
  * cores with fp32 accumulation, E4M3 codes converted exactly; weights are rounded before the second
