@@ -386,3 +386,24 @@ def test_graph_and_streams():
         got = run(side)
         side.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("T,H,D", [(1, 1, 32), (17, 5, 96), (40, 3, 128), (3, 2, 512)])
+def test_mxfp4_codes(dtype, T, H, D):
+    """Nibble by nibble: the even value in the low one, codes to nearest even and saturating, on values half way between
+    two codes and on borders of the exponent too.  A zero's sign is free."""
+    g = torch.Generator().manual_seed(T * D)
+    x = torch.randn((T, H, D), generator=g) * torch.exp2(torch.randint(-9, 10, (T, H, 1), generator=g).float())
+    ties = torch.tensor([0.25, -0.75, 1.25, -1.75, 2.5, -3.5, 5.0, 7.0])
+    x[-1, -1, :8] = ties * 4.0                 # amax 28: unit 4
+    x[-1, -1, 8:32] = 0.0
+    x = x.to(dtype)
+    c = idx.Cache.empty(T, H, D, FP4)
+    idx.idx_cache_write([idx.Write(x.cuda(), c)])
+    packed, e8 = quantise_mxfp4(x.float().numpy())
+    assert np.array_equal(c.scale.cpu().numpy(), e8)
+    got = c.data.cpu().numpy()
+    for shift in (0, 4):
+        a, b = (got >> shift) & 15, (packed >> shift) & 15
+        assert ((a == b) | ((a | b) == 8)).all()
