@@ -116,9 +116,10 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 // Memory-to-LDS copies: lane l's 16 (4) bytes land at LDS byte lds + 16 l (4 l); lds is wave-uniform and goes
-// through m0, which nothing else here uses.  The compiler does not count them, so the kernel waits itself:
-// copies and loads of a wave complete in the order of their issue, so with at most N operations under way
-// every copy is there that N others certainly followed; more of them only make the wait stricter.
+// through m0, which the compiler reserves (it warns of a clobber) and no other instruction here reads.  The
+// compiler does not count the copies, so the kernel waits itself: copies and loads of a wave complete in the order of
+// their issue, so with at most N operations under way every copy is there that N others certainly followed; more of
+// them only make the wait stricter.
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 __device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(uintptr_t)(const lds_u8 *)p; }
 __device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds) {
@@ -150,9 +151,12 @@ constexpr int wave_lds(bool fp8, int D, bool wide) {
   return 2 * TILE * (fp8 ? D : 2 * D) + 4 * QUEUE * (fp8 && !wide ? 2 : 1) + (fp8 ? 8 * TILE : 0);
 }
 
-// Waves a SIMD that the registers allow, asked for so that a register more does not cost one (E4M3, 128 dims, 600 rows
-// x 4 cache heads: 63 us with three, 70 with two).
-constexpr int waves_a_simd(bool fp8, int D, int mt) { return (D == 64 ? 3 : 2) + (mt == 1 && (fp8 || D == 64) ? 1 : 0); }
+// Waves a SIMD, asked for so that a register more does not cost one (E4M3, 128 dims, 600 rows x 4 cache heads: 63 us
+// with three, 70 with two).  The registers allow them but for 16-bit rows of 64 dims, whose kernels keep one register
+// (16 heads) or six (32) in scratch memory while the tiles run: stored before their loop, loaded behind it.
+constexpr int waves_a_simd(bool fp8, int D, int mt) {
+  return (D == 64 ? 3 : 2) + (mt == 1 && (fp8 || D == 64) ? 1 : 0);
+}
 
 // BF16: q's type; FP8: E4M3 caches (else of q's type); MT: 16-head tiles.
 // WIDE: caches past 2^32 bytes (64-bit offsets of rows instead of 32-bit ones beside a uniform base).
@@ -688,8 +692,9 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   // 32 heads to a wave where rows alone nearly fill the machine (2 waves a SIMD): each key is fetched once for them.
   // From 768 waves on 32 heads are as fast or faster with 24, 32 and 64 query heads, 64 and 128 dims, 512 and 2048
   // keys, either type of cache.  us with 16 heads a wave and with 32, 2048 keys, 32 heads of 128 and of 64: E4M3,
-  // 512 rows 53, 82 and 41, 63; 768 rows 81, 83 and 64, 63; 1024 rows 90, 83 and 67, 63; 2048 rows 160, 123 and 127, 90; bf16,
-  // 512 rows 53, 58 and 31, 47; 768 rows 75, 57 and 46, 47; 1024 rows 90, 60 and 52, 49; 2048 rows 171, 99 and 97, 65
+  // 512 rows 53, 82 and 41, 63; 768 rows 81, 83 and 64, 63; 1024 rows 90, 83 and 67, 63; 2048 rows 160, 123 and 127,
+  // 90; bf16, 512 rows 53, 58 and 31, 47; 768 rows 75, 57 and 46, 47; 1024 rows 90, 60 and 52, 49; 2048 rows 171, 99
+  // and 97, 65
   p.tiles = G > 16 && (int64_t)T * Hkv * ((G + 31) / 32) >= 768 ? 2 : 1;
   const int32_t heads = 16 * p.tiles;
   p.blocks = (G + heads - 1) / heads;
@@ -714,12 +719,12 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
     }
   } else if (p.tiles == 1 && items <= 384 && tiles > 32 && Hkv > 1 && touched > FROM_MEMORY) {
     // More items than CUs, and up to one and a half: a workgroup each leaves some CUs twice the others' share of what
-    // memory brings, and the heads of a slot, which lie together, are read apart.  2048 keys of 128 dims through a slot
-    // table, us, four workgroups of a wave and one of four, E4M3 and bf16: 33 rows x 8 cache heads 47, 53 and 68, 76;
-    // 40 rows 51, 63 and 75, 80; 48 rows 59, 65 and 87, 85; 96 rows x 4 58, 60 and 89, 86; 180 rows x 2 56, 57 and 81,
-    // 80 (slots in order: 51, 47 and 81, 78).  Past it a workgroup each is as fast or faster (52 rows x 8 66, 67 and 95,
-    // 88), and so it is for one cache head (400 rows of 16 heads 78, 66 and 95, 84), rows that a cache on the chip holds
-    // (300 of 16 heads 35, 26) and shorter lists (33 rows x 8, 512 keys: 17.5, 15.5)
+    // memory brings.  2048 keys of 128 dims through a slot table, us, four workgroups of a wave and one of four, E4M3
+    // and bf16: 33 rows x 8 cache heads 47, 53 and 68, 76; 40 rows 51, 63 and 75, 80; 48 rows 59, 65 and 87, 85; 96 rows
+    // x 4 58, 60 and 89, 86; 180 rows x 2 56, 57 and 81, 80 (slots in order: 51, 47 and 81, 78).  Past it a workgroup
+    // each is as fast or faster (52 rows x 8 66, 67 and 95, 88), and so it is for one cache head (400 rows of 16 heads
+    // 78, 66 and 95, 84), rows that a cache on the chip holds (300 of 16 heads 35, 26) and shorter lists (33 rows x 8,
+    // 512 keys: 17.5, 15.5)
     p.splits = 4;
   } else if (p.tiles == 1) {
     // Two or four waves to a workgroup while all fit the machine about at once (LDS and registers: 2048 waves of

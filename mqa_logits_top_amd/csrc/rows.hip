@@ -5,7 +5,7 @@
 // Both move each byte once.  Measured (a large copy moves 4.9 TB/s here, reads and writes counted):
 //   16384 rows x 64 heads of 128 rotated, bf16: 93 us, 5.8 TB/s (the copy's rate: 110 us);
 //   30720 rows x 8 heads, keys rotated and values, to E4M3 slots in any order: 48 us, 4.0 TB/s (39 us);
-//   2048 rows x 64 heads rotated to E4M3: 16 us (10.5 us): the lanes' loads are all under way at once, and the
+//   2048 rows x 64 heads rotated to E4M3: 17 us (10.5 us): the lanes' loads are all under way at once, and the
 //     800 instructions of a wave follow them;
 //   102400 MXFP4 rows read: 8.1 us, 4.1 TB/s (6.9 us); one row of 32 heads rotated: 2.9 us, the launch.
 #include "common.h"
@@ -125,11 +125,11 @@ __device__ __forceinline__ float inverse_rest(float amax, float inv) {
   return __builtin_fmaf(-inv, amax, 448.0f) * (inv * (1.0f / 448.0f));
 }
 
-// Sine and cosine of an angle below 2^32, within a few 2^-50: the angle less its nearest multiple of pi/2
-// (pi/2 in three parts of 53 bits; each fma is exact but for its one rounding, and the angle's multiple k of
-// pi/2 is below 2^32), then the Taylor series of sine and cosine on [-pi/4, pi/4] (terms dropped: below
-// 2^-45 of 1) and the quadrant's exchange of the two.  No branch, a quarter of the library function's
-// instructions, which took more time than the rotation.
+// Sine and cosine of an angle below 2^32, within 2^-45 (fp32 keeps 2^-24): the angle less its nearest multiple of
+// pi/2 (pi/2 in three parts of 53 bits; each fma is exact but for its one rounding, and the angle's multiple k of
+// pi/2 is below 2^32), then the Taylor series on [-pi/4, pi/4], the sine's to x^13 (the next term is below 2^-45.4),
+// the cosine's to x^14 (2^-49.7), and the quadrant's exchange of the two.  No branch, a quarter of the library
+// function's instructions, which took more time than the rotation.
 __device__ __forceinline__ void sin_cos(double x, double *sn, double *cs) {
   const double k = __builtin_rint(x * 0.63661977236758134308);   // 2 / pi
   double r = __builtin_fma(-k, 1.57079632679489655800, x);
