@@ -436,7 +436,8 @@ idx_status idx_cache_read(const idx_cache *c, const int32_t *rows, const idx_row
  * alike, with the same slots and strides; D = 64 or 128; T * Hq below 2^26.  Products run on the matrix
  * cores with fp32 accumulation, E4M3 codes converted exactly; weights are rounded before the second
  * product (by at most 2^-8 of their value in bf16; 2^-11 in fp16, and 2^-32 of the row's largest weight for
- * those below 2^-21 of it; 2^-16 for either type with E4M3 caches), sums and maxima are fp32.
+ * those below 2^-21 of it; 2^-16 for either type with E4M3 caches), sums and maxima are fp32.  The sums are
+ * divided last: bf16 or E4M3 values within a factor of 2^8 n_sel pool of fp32's largest number can overflow them.
  * ws: idx_sparse_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap
  * in time need one each. */
 typedef struct idx_attn {

@@ -45,6 +45,7 @@ constexpr int MAX_WAVES = 8;  // of a workgroup
 constexpr int MAX_SPLITS = 256;
 constexpr int64_t FROM_MEMORY = (int64_t)128 << 20;   // bytes: half of the last cache
 constexpr float NEG_INF = -__builtin_inff();
+constexpr float BIG = 0x1p20f;   // references from which on a score is rounded before the reference is taken off
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -103,6 +104,11 @@ __device__ __forceinline__ float head_sum(float x) {
   return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// A product rounded by itself, never part of an fma.
+__device__ __forceinline__ float product(float x, float y) {
+#pragma clang fp contract(off)
+  return x * y;
+}
 __device__ __forceinline__ float max8(const float *x) {
   float m = x[0];
 #pragma unroll
@@ -152,8 +158,8 @@ constexpr int wave_lds(bool fp8, int D, bool wide) {
 }
 
 // Waves a SIMD, asked for so that a register more does not cost one (E4M3, 128 dims, 600 rows x 4 cache heads: 63 us
-// with three, 70 with two).  The registers allow them but for 16-bit rows of 64 dims, whose kernels keep one register
-// (16 heads) or six (32) in scratch memory while the tiles run: stored before their loop, loaded behind it.
+// with three, 70 with two).  The registers do not quite allow them in some variants, which keep one to three in scratch
+// memory while the tiles run: stored before their loop, loaded behind it.
 constexpr int waves_a_simd(bool fp8, int D, int mt) {
   return (D == 64 ? 3 : 2) + (mt == 1 && (fp8 || D == 64) ? 1 : 0);
 }
@@ -438,8 +444,13 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D,
       // The reference (LIFT below the largest score) moves only when a score is 2^8 above that: the
       // accumulators are rescaled a few times a row instead of at most tiles.  The four lanes of a head
       // share their reference, so a lane's own scores decide whether there is anything to do.
-      if (__any(top > ref[m] + (8.f + LIFT))) {
+      // A large reference itself is off by more than the exponential's range (by 2^7 from 2^31 on), so that one fma a
+      // weight, exact in the product, would leave infinities or zeros: from BIG on, which is looked at in every
+      // tile then, the products are rounded like the reference.
+      bool big = false;
+      if (__any(top > (__builtin_fabsf(ref[m]) < BIG ? ref[m] + (8.f + LIFT) : NEG_INF))) {
         const float to = __builtin_fmaxf(ref[m], head_max(top) - LIFT);
+        big = __any(__builtin_fabsf(to) >= BIG);
         const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
         sum[m] *= f;
         rounded[m] *= f;
@@ -448,10 +459,18 @@ __global__ __launch_bounds__(MT == 1 ? 64 * MAX_WAVES : 64, waves_a_simd(FP8, D,
         ref[m] = to;
         neg[m] = to == NEG_INF ? 0.f : -to;
       }
+      if (big) {
+        asm volatile("");   // stays a branch
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[m][i] = product(sc[m][i], a.scale2) + neg[m];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sc[m][i] = __builtin_fmaf(sc[m][i], a.scale2, neg[m]);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float x = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[m][2 * i], a.scale2, neg[m]));
-        float y = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[m][2 * i + 1], a.scale2, neg[m]));
+        float x = __builtin_amdgcn_exp2f(sc[m][2 * i]);
+        float y = __builtin_amdgcn_exp2f(sc[m][2 * i + 1]);
         sum[m] += x + y;
         if constexpr (FP8) {
           x *= vsc[2 * i];

@@ -68,3 +68,45 @@ def test_many_small_weights(dtype, first, T, Hq, D, n):
     err = np.abs(out.cpu().double().numpy() - want)
     assert (err <= bound).all(), f"{(err > bound).sum()} off, worst {np.max(err / bound):.2f} of the bound"
     assert np.abs(lse.cpu().double().numpy() - np.log(w.sum())).max() <= 2.0 ** -19 + n * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype,fp8,power", [(torch.bfloat16, False, p) for p in (20, 30, 40, 90)]
+                         + [(torch.float16, False, p) for p in (18, 22, 26)]
+                         + [(torch.bfloat16, True, p) for p in (20, 30, 40, 90)]
+                         + [(torch.float16, True, p) for p in (18, 30, 40)])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("T,Hq,D,n", [(1, 8, 64, 3000), (200, 16, 128, 600), (800, 32, 64, 300), (800, 32, 128, 300)])
+def test_large_scores(dtype, fp8, power, sign, T, Hq, D, n):
+    """Scores of 9, 11, 13 and 15 times D 2^power and a factor of each head's, products exact in fp32: the keys of the
+    largest share the weight alike and the others, 30000 or more below in the exponent, have none."""
+    rng = np.random.default_rng(power + n)
+    half = power // 2 if dtype == torch.bfloat16 else power - 14
+    size = rng.choice([9, 11, 13, 15], n)
+    size[: n // 3] = 11                                                 # the largest comes late
+    key = torch.from_numpy(sign * size * 2.0 ** half)[:, None, None].expand(n, 1, D)
+    val = torch.from_numpy(rng.integers(-8, 9, (n, 1, D)) * 0.5)
+    caches = []
+    for x in (key, val):
+        c = idx.Cache.empty(n, 1, D, FP8 if fp8 else idx.IDX_K_F16 if dtype == torch.float16 else idx.IDX_K_BF16)
+        if fp8:                                                         # exact: codes of 4 bits, scales a power of two
+            top = x.abs().amax(-1).clamp(min=0.5)
+            unit = torch.exp2(torch.floor(torch.log2(top)))
+            c.data.copy_((x / unit[..., None]).to(torch.float8_e4m3fn).view(torch.uint8))
+            c.scale.copy_(unit)
+        else:
+            c.data.copy_(x)
+        caches.append(c)
+    factor = 2.0 ** (power - half) * (1 + torch.arange(Hq, dtype=torch.float64) % 16 / 16)
+    q = factor[:, None].expand(T, Hq, D).to(dtype).cuda()
+    scale = 0.1 * 2.0 ** -0.5
+    sel = torch.arange(n, dtype=torch.int32, device="cuda").expand(T, n).contiguous()
+    out, lse = idx.idx_sparse_attn(q, *caches, sel, scale)
+    best = size == (size * sign).max() * sign
+    want = val[torch.from_numpy(best)][:, 0].mean(0)
+    # equal weights, rounded alike; sums of n products in fp32; the result's rounding
+    half_step = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -11
+    bound = half_step * want.abs() + (2.0 ** -16 + 2.0 ** -21 + n * 2.0 ** -23) * 4.0
+    assert ((out.cpu().double() - want).abs() <= bound).all()
+    s = float(np.float32(scale)) * sign * size[best][0] * factor * D * 2.0 ** half
+    # the score: its factor rounded twice, itself once, the logarithm's share in fp32 steps of it
+    assert ((lse.cpu().double() - (s + np.log(best.sum()))).abs() <= 2.0 ** -21 * s.abs()).all()
