@@ -22,8 +22,8 @@
 // however few they are in memory.  D = 128, 2 waves a SIMD by registers.
 //   2048 rows x 2048 of 65536 keys, 32 heads on one bf16 cache head: 100 us, 690 TFLOP/s (58 us at the rate of a
 //     large product); 2.1 GB through the L2s at 21 TB/s, which reach 27 with nothing but such loads (80 us).
-//   2048 rows x 512 of 102400, 64 heads, E4M3: 73 us, 470 TFLOP/s (29 us): vector instructions, conversions of codes
-//     and of weights first among them, and matrix instructions, half as many again for the weights' second part.
+//   2048 rows x 512 of 102400, 64 heads, E4M3: 73 us, 470 TFLOP/s (29 us): vector instructions, nearly half of
+//     them conversions of codes and of weights, and matrix instructions, a third of them for the weights' second part.
 //   40 rows x 2048 of 4000 each, 32 heads on 8, E4M3, paged: 48 us, 3.6 TB/s (36 us): scattered 1 KB slots.
 //   1023 rows x 96 blocks of 8 keys, 16 heads of 64 on 2, fp16: 22 us: 0.4 GB gathered at 18 TB/s.
 //   1 row x 512 keys, 64 heads, bf16: 8.4 us, of which 3.6 are a launch and the rest three loads' latencies in turn
@@ -739,11 +739,11 @@ AttnPlan plan_attn(int32_t T, int32_t Hkv, int32_t G, int32_t D, bool fp8, int64
   } else if (p.tiles == 1 && items <= 384 && tiles > 32 && Hkv > 1 && touched > FROM_MEMORY) {
     // More items than CUs, and up to one and a half: a workgroup each leaves some CUs twice the others' share of what
     // memory brings.  2048 keys of 128 dims through a slot table, us, four workgroups of a wave and one of four, E4M3
-    // and bf16: 33 rows x 8 cache heads 47, 53 and 68, 76; 40 rows 51, 63 and 75, 80; 48 rows 59, 65 and 87, 85; 96 rows
-    // x 4 58, 60 and 89, 86; 180 rows x 2 56, 57 and 81, 80 (slots in order: 51, 47 and 81, 78).  Past it a workgroup
-    // each is as fast or faster (52 rows x 8 66, 67 and 95, 88), and so it is for one cache head (400 rows of 16 heads
-    // 78, 66 and 95, 84), rows that a cache on the chip holds (300 of 16 heads 35, 26) and shorter lists (33 rows x 8,
-    // 512 keys: 17.5, 15.5)
+    // and bf16: 33 rows x 8 cache heads 47, 53 and 68, 76; 40 rows 51, 63 and 75, 80; 48 rows 59, 65 and 87, 85; 96
+    // rows x 4 58, 60 and 89, 86; 180 rows x 2 56, 57 and 81, 80 (slots in order: 51, 47 and 81, 78).  Past it a
+    // workgroup each is as fast or faster (52 rows x 8 66, 67 and 95, 88), and so it is for one cache head (400 rows of
+    // 16 heads 78, 66 and 95, 84), rows that a cache on the chip holds (300 of 16 heads 35, 26) and shorter lists
+    // (33 rows x 8, 512 keys: 17.5, 15.5)
     p.splits = 4;
   } else if (p.tiles == 1) {
     // Two or four waves to a workgroup while all fit the machine about at once (LDS and registers: 2048 waves of
