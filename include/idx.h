@@ -457,6 +457,69 @@ typedef struct idx_attn {
 idx_status idx_sparse_attn_workspace(const idx_attn *a, size_t *bytes);
 idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *stream);
 
+/* Attention of the new rows of a batch over every key of their requests, in a paged cache.  Request b owns the rows
+ * [cu_q[b], cu_q[b + 1]), which are the last of its len_k[b] keys: row i of n (from 0) is at position
+ * p = len_k[b] - n + i and sees the keys 0 .. p, or with window > 0 the keys s with p - window < s <= p and those with
+ * s < min(first, p + 1):
+ *     out[t, h, :] = sum_s w_s v[slot(s), h / G, :],  w = softmax_s(scale * <q[t, h, :], k[slot(s), h / G, :]>),
+ *     slot(s) = pages[b * ld_pages + s / page] * page + s % page,
+ * G = Hq / H consecutive query heads to a cache head.  lse (nullable): [T, Hq] fp32, ln of the sum of the exponentials.
+ * A row that sees no key (p < 0, as where len_k[b] is short of the request's rows) gets zeros and -inf.  Rows in no
+ * request (before cu_q[0], at or behind cu_q[B]) are left as they are, in out and in lse.  One row a request is a decode
+ * step; requests of any lengths, zero among them, share a call.
+ * cu_q (not descending, within [0, T]), len_k and pages are read on the device: the call can be captured and replayed with
+ * other lengths in them, and is sized by T, B and n_pages * page, which bounds len_k (a longer one is taken as that).
+ * A key whose slot is outside the caches does not count.  Slots that no row of a request sees are not read, or read and
+ * not used: what they hold reaches no output.  A value that is not finite reaches the rows that see its key and no
+ * others.  IDX_DEBUG checks cu_q, len_k and the pages that the lengths reach.
+ * Types, head sizes and layouts are those of idx_sparse_attn, and so are scores, sums and maxima (fp32).  Weights are
+ * rounded to 16 bits before the second product: by at most 2^-8 of their value with bf16 q; with fp16 q by 2^-11, and 2^-32
+ * of the row's largest weight for those below 2^-21 of it, or 2^-16 with E4M3 caches (where a weight is the product with
+ * its value's scale).
+ * The sums are divided last: values within a factor of 2^8 len_k of fp32's largest number can overflow them.
+ * A call's results are bitwise repeatable; a row's bits depend on the sizes and lengths of the call, by which its keys
+ * are divided, and not on what other rows hold.
+ * page: a power of two; n_pages * page below 2^31; B up to 2^16; T * Hq below 2^26.
+ * ws: idx_paged_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap in time need one
+ * each. */
+typedef struct idx_paged {
+  idx_rows q;
+  idx_rows out;
+  idx_cache k, v;
+  const int32_t *pages;         /* [B, n_pages], row b at b * ld_pages */
+  int64_t ld_pages;
+  int32_t n_pages, page;
+  const int32_t *cu_q;          /* [B + 1] */
+  const int32_t *len_k;         /* [B]     */
+  int32_t B;
+  int32_t window, first;        /* window 0: every key up to the row's own; first is not read then */
+  float scale;
+  float *lse;                   /* nullable */
+} idx_paged;
+idx_status idx_paged_attn_workspace(const idx_paged *a, size_t *bytes);
+idx_status idx_paged_attn(const idx_paged *a, void *ws, size_t ws_bytes, void *stream);
+
+/* Root-mean-square norm of each of the T x H rows of D values, the residual added before it:
+ *     h = x + residual (fp32),  total = h rounded to its type,  y = h / sqrt(mean(h^2) + eps) * weight,
+ *     out = y rounded to its type, and / or y as E4M3 codes with scales in the slots 0 .. T - 1 of `to`.
+ * The norm takes the sum as it is before total's rounding.  A hidden row has H = 1 and D values; then `to` may hold it as
+ * to->H groups of to->D values with a scale each (to->H * to->D = D).  With H > 1 (each head of a query or a key) to->H = H
+ * and to->D = D.  Codes and scales are idx_cache_write's, from y in fp32 (a group that holds a NaN or an infinity reads back
+ * as NaN).  The row's squares are summed in fp32; a row whose sum overflows gives zeros, and NaN for its infinities.
+ * x, out and weight are of any value types, residual and total of one; out has x's sizes.  residual.data NULL: none, and
+ * total is not read.  out.data NULL: codes only; to NULL: values only; one of them is given.  total may be residual or x
+ * itself, and out may be x, residual (with another total) or, for codes only, absent; in place the strides are the same.
+ * Otherwise outputs share no byte with inputs or with each other.
+ * D a multiple of 8, at most 32768; groups smaller than a row are 8, 16, 32, ... 512 values; T * H below 2^31 / 64. */
+typedef struct idx_norm {
+  idx_rows x, residual, total, out;
+  const idx_cache *to;          /* nullable; read during the call only */
+  const void *weight;           /* [D], nullable: ones                 */
+  int32_t weight_dtype;         /* a value type                        */
+  float eps;                    /* >= 0                                */
+} idx_norm;
+idx_status idx_rms_norm(const idx_norm *n, void *stream);
+
 /* Launch timing, for benchmarks and profilers (P3: the chunk-budget and CPU-gap
  * commits attribute the indexer's time to its kernels).  idx_launch_timing(1) clears
  * the record and starts recording on the current device: from then on each scoring

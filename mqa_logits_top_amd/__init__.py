@@ -8,8 +8,8 @@ missing or fails to load, every call raises.
 
 Function names match the C entry points.  Tensors must be on the GPU and
 contiguous; key indices in outputs are absolute rows of k.  The operators around
-the indexer (idx_rope, idx_cache_write, idx_cache_read, idx_sparse_attn) check
-types, shapes and devices here, and take any strides the C entry points take.
+the indexer (idx_rope, idx_cache_write, idx_cache_read, idx_sparse_attn,
+idx_paged_attn, idx_rms_norm) check types, shapes and devices here, and take any strides the C entry points take.
 They record no gradient and refuse rows that require one while autograd is on.
 """
 from __future__ import annotations
@@ -51,7 +51,8 @@ EXPORTS = ("idx_mqa_logits", "idx_mqa_logits_block", "idx_topk", "idx_logits_top
            "idx_refine_topk",
            "idx_block_candidates", "idx_workspace_size", "idx_ragged_windows", "idx_ragged_windows_ratio",
            "idx_gather_rows", "idx_tail_rows", "idx_rope_freqs", "idx_rope", "idx_cache_write", "idx_cache_read",
-           "idx_sparse_attn_workspace", "idx_sparse_attn", "idx_launch_timing", "idx_launch_timing_read",
+           "idx_sparse_attn_workspace", "idx_sparse_attn", "idx_paged_attn_workspace", "idx_paged_attn", "idx_rms_norm",
+           "idx_launch_timing", "idx_launch_timing_read",
            "idx_status_str")
 
 IDX_TIMING_MAX = 1024
@@ -106,6 +107,20 @@ class idx_attn(ctypes.Structure):
                 ("L", ctypes.c_int32), ("scale", ctypes.c_float), ("lse", ctypes.c_void_p)]
 
 
+class idx_paged(ctypes.Structure):
+    _fields_ = [("q", idx_rows), ("out", idx_rows), ("k", idx_cache), ("v", idx_cache), ("pages", ctypes.c_void_p),
+                ("ld_pages", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("cu_q", ctypes.c_void_p), ("len_k", ctypes.c_void_p), ("B", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("first", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("lse", ctypes.c_void_p)]
+
+
+class idx_norm(ctypes.Structure):
+    _fields_ = [("x", idx_rows), ("residual", idx_rows), ("total", idx_rows), ("out", idx_rows),
+                ("to", ctypes.POINTER(idx_cache)), ("weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -141,6 +156,9 @@ def load_library():
     lib.idx_cache_read.argtypes = [C, VP, R, VP]
     lib.idx_sparse_attn_workspace.argtypes = [ctypes.POINTER(idx_attn), ctypes.POINTER(sz)]
     lib.idx_sparse_attn.argtypes = [ctypes.POINTER(idx_attn), VP, sz, VP]
+    lib.idx_paged_attn_workspace.argtypes = [ctypes.POINTER(idx_paged), ctypes.POINTER(sz)]
+    lib.idx_paged_attn.argtypes = [ctypes.POINTER(idx_paged), VP, sz, VP]
+    lib.idx_rms_norm.argtypes = [ctypes.POINTER(idx_norm), VP]
     lib.idx_launch_timing.argtypes = [i32]
     lib.idx_launch_timing_read.argtypes = [ctypes.POINTER(idx_launch_time), i32, ctypes.POINTER(i32)]
     lib.idx_status_str.argtypes = [i32]
@@ -787,3 +805,114 @@ def idx_sparse_attn(q: torch.Tensor, k: Cache, v: Cache, sel: torch.Tensor, scal
     if s:
         raise IdxError("idx_sparse_attn", s)
     return out, lse
+
+
+def idx_paged_attn(q: torch.Tensor, k: Cache, v: Cache, pages: torch.Tensor, cu_q: torch.Tensor, len_k: torch.Tensor,
+                   scale: float, page: int, window: int = 0, first: int = 0, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, with_lse: bool = True,
+                   stream=None):
+    """Attention of the new rows q [T, Hq, D] of a batch over the keys of their requests, or over the last `window`
+    and the `first` of them; (out, lse).  Request b has the rows cu_q[b] .. cu_q[b + 1] - 1, the last of its len_k[b]
+    keys, which lie in the slots pages[b] names, `page` to a page."""
+    device, rows = k.device, _rows(q, "q")
+    T, Hq = rows.T, rows.H
+    if q.device != device or v.device != device:
+        raise ValueError(f"caches on {k.device} and {v.device} for q on {q.device}")
+    if (pages.dtype is not torch.int32 or pages.device != device or pages.dim() != 2
+            or (pages.stride(1) != 1 and pages.shape[1] > 1)):
+        raise ValueError(f"pages: [B, n] int32 on {device} with a contiguous last dimension, got {list(pages.shape)} "
+                         f"{pages.dtype} on {pages.device}")
+    B = pages.shape[0]
+    if cu_q.shape != (B + 1,) or len_k.shape != (B,):
+        raise ValueError(f"cu_q: [{B + 1}] and len_k: [{B}] for {B} rows of pages, got {list(cu_q.shape)} and "
+                         f"{list(len_k.shape)}")
+    a_cu, a_len = _on(cu_q, device, torch.int32, "cu_q"), _on(len_k, device, torch.int32, "len_k")
+    lib = load_library()
+    with _on_stream(device, stream) as st:
+        if out is None:
+            out = q.new_empty(q.shape)
+            to = _new_rows(out, rows.dtype, *q.shape)
+        elif out.device != device:
+            raise ValueError(f"out on {out.device} for q on {device}")
+        else:
+            to = _rows(out, "out")
+        if lse is None:
+            if with_lse:
+                lse = q.new_empty((T, Hq), dtype=torch.float32)
+        elif lse.shape != (T, Hq):
+            raise ValueError(f"lse: {[T, Hq]}")
+        a = idx_paged(rows, to, k._struct, v._struct, pages.data_ptr(), pages.stride(0), pages.shape[1], page, a_cu, a_len,
+                      B, window, first, scale, None if lse is None else _on(lse, device, torch.float32, "lse"))
+        at, size = None, 0
+        if ws is None:
+            need = ctypes.c_size_t()
+            s = lib.idx_paged_attn_workspace(a, need)
+            if s:
+                raise IdxError("idx_paged_attn_workspace", s)
+            size = need.value
+            if size:
+                ws = torch.empty(size, dtype=torch.uint8, device=device)
+        else:
+            size = ws.numel()
+        if ws is not None:
+            at = _on(ws, device, torch.uint8, "ws")
+        s = lib.idx_paged_attn(a, at, size, st)
+    if s:
+        raise IdxError("idx_paged_attn", s)
+    return out, lse
+
+
+def _norm_rows(x: torch.Tensor, what: str) -> idx_rows:
+    """Rows [T, H, D], or hidden rows [T, D] as one head."""
+    if x.dim() == 2:
+        x = x.unsqueeze(1)
+    return _rows(x, what)
+
+
+def idx_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 residual: Optional[torch.Tensor] = None, total: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, to: Optional[Cache] = None, with_out: bool = True, stream=None):
+    """RMS norm of each row of x [T, D], or of each head of x [T, H, D], times weight [D]; returns out (None where
+    with_out is False).  residual: added before the norm, the sum written to `total`, or to the residual itself where that
+    is None.  to: an E4M3 cache of T slots or more that receives the result with a scale for each of its heads, which for
+    x [T, D] may be groups of D."""
+    rows, device = _norm_rows(x, "x"), x.device
+    none = idx_rows()
+    r = t = none
+    if residual is not None:
+        total = residual if total is None else total
+        if residual.shape != x.shape or total.shape != x.shape:
+            raise ValueError(f"residual and total: {list(x.shape)} as x, got {list(residual.shape)} and {list(total.shape)}")
+        if residual.device != device or total.device != device:
+            raise ValueError(f"residual on {residual.device} and total on {total.device} for x on {device}")
+        r, t = _norm_rows(residual, "residual"), _norm_rows(total, "total")
+    elif total is not None:
+        raise ValueError("total without a residual")
+    w, w_type = None, IDX_K_F32
+    if weight is not None:
+        if weight.requires_grad and torch.is_grad_enabled():
+            raise ValueError("weight requires a gradient, and no entry point records one: call it under torch.no_grad() "
+                             "or on weight.detach()")
+        if weight.shape != x.shape[-1:] or weight.dtype not in _VALUE:
+            raise ValueError(f"weight: {list(x.shape[-1:])} bfloat16, float16 or float32, got {list(weight.shape)} "
+                             f"{weight.dtype}")
+        w, w_type = _on(weight, device, weight.dtype, "weight"), _VALUE[weight.dtype]
+    codes = None
+    if to is not None:
+        if to.device != device:
+            raise ValueError(f"a cache on {to.device} for x on {device}")
+        codes = ctypes.pointer(to._struct)
+    with _on_stream(device, stream) as st:
+        if out is not None:
+            if out.device != device or out.shape != x.shape:
+                raise ValueError(f"out: {list(x.shape)} on {device}, got {list(out.shape)} on {out.device}")
+            o = _norm_rows(out, "out")
+        elif with_out:
+            out = x.new_empty(x.shape)
+            o = _new_rows(out, rows.dtype, rows.T, rows.H, rows.D)
+        else:
+            o = none
+        s = load_library().idx_rms_norm(idx_norm(rows, r, t, o, codes, w, w_type, eps), st)
+    if s:
+        raise IdxError("idx_rms_norm", s)
+    return out

@@ -1,5 +1,5 @@
 // C ABI of the operators around the indexer: rotary positions, cache writes and reads, attention
-// over the selection.  Argument checks and launch descriptions, as in api.cpp.
+// over the selection and over paged caches, the RMS norm.  Argument checks and launch descriptions, as in api.cpp.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -9,12 +9,17 @@
 #include "../../include/idx.h"
 #include "api_internal.h"
 #include "attn.h"
+#include "norm.h"
+#include "paged.h"
 #include "rows.h"
 
 namespace {
 
 constexpr int32_t MAX_D = 512;
 constexpr int32_t MAX_ROT = 512;
+constexpr int32_t MAX_NORM = 32768;
+constexpr int32_t MAX_GROUP = 512;             // values with a scale of their own, where a row has several
+constexpr int32_t MAX_REQUESTS = 1 << 16;
 constexpr int32_t MAX_POOL = 64;
 constexpr int64_t MAX_LD = (int64_t)1 << 31;   // strides: their products with 32-bit counts stay inside 64 bits
 constexpr int64_t MAX_ROW = (int64_t)1 << 30;  // elements of an attention cache's slot: 32 bits of bytes
@@ -36,10 +41,10 @@ int bits(int32_t fmt) {
 bool value_type(int32_t f) { return f == IDX_K_BF16 || f == IDX_K_F16 || f == IDX_K_F32; }
 
 // Rows of values; written: rows may not share memory.
-idx_status check_rows(const idx_rows &x, bool written) {
+idx_status check_rows(const idx_rows &x, bool written, int32_t max_d = MAX_D) {
   if (x.T < 0 || x.H < 0 || x.D <= 0) return IDX_E_SHAPE;
   if (!value_type(x.dtype)) return IDX_E_FORMAT;
-  if (x.D % 8 || x.D > MAX_D) return IDX_E_UNSUPPORTED;
+  if (x.D % 8 || x.D > max_d) return IDX_E_UNSUPPORTED;
   if (x.ld_t < 0 || x.ld_h < 0 || x.ld_t > MAX_LD || x.ld_h > MAX_LD) return IDX_E_SHAPE;
   if (x.T == 0 || x.H == 0) return IDX_OK;
   if (!x.data) return IDX_E_NULL;
@@ -53,11 +58,11 @@ idx_status check_rows(const idx_rows &x, bool written) {
   return IDX_OK;
 }
 
-idx_status check_cache(const idx_cache &c) {
+idx_status check_cache(const idx_cache &c, int32_t max_d = MAX_D) {
   if (c.rows < 0 || c.rows > INT32_MAX || c.H <= 0 || c.D <= 0) return IDX_E_SHAPE;
   const int b = bits(c.fmt);
   if (!b) return IDX_E_FORMAT;
-  if (c.D % (c.fmt == IDX_K_MXFP4 ? 32 : 8) || c.D > MAX_D) return IDX_E_UNSUPPORTED;
+  if (c.D % (c.fmt == IDX_K_MXFP4 ? 32 : 8) || c.D > max_d) return IDX_E_UNSUPPORTED;
   const int64_t width = (int64_t)c.H * c.D;
   const bool scaled = c.fmt == IDX_K_FP8_E4M3 || c.fmt == IDX_K_MXFP4;
   const int64_t swidth = c.fmt == IDX_K_MXFP4 ? width / 32 : c.H;
@@ -124,10 +129,11 @@ int64_t lanes_of(const idx_rows &x) {
 }
 
 // The scale for powers of two.
-float scale2_of(const idx_attn *a) { return (float)((double)a->scale * 1.4426950408889634); }
+float scale2_of(float scale) { return (float)((double)scale * 1.4426950408889634); }
 
-idx_status check_attn(const idx_attn *a) {
-  if (!a) return IDX_E_NULL;
+// Queries, outputs and caches of an attention.
+template <class Attn>
+idx_status check_attn_arrays(const Attn *a) {
   idx_status st;
   if ((st = check_rows(a->q, false)) || (st = check_rows(a->out, true))) return st;
   if ((st = check_cache(a->k)) || (st = check_cache(a->v))) return st;
@@ -140,20 +146,90 @@ idx_status check_attn(const idx_attn *a) {
   if (a->q.D != 64 && a->q.D != 128) return IDX_E_UNSUPPORTED;
   if (a->k.ld != a->v.ld || a->k.ld_scale != a->v.ld_scale) return IDX_E_SHAPE;
   if (a->k.ld > MAX_ROW) return IDX_E_UNSUPPORTED;
+  if ((int64_t)a->q.T * a->q.H >= (int64_t)1 << 26) return IDX_E_UNSUPPORTED;   // at most a wave each: 2^32 lanes
+  if (!std::isfinite(scale2_of(a->scale))) return IDX_E_PARAM;
+  // the attention kernels read 16 bytes of a cache row at a time
+  const int64_t per = 128 / bits(a->k.fmt);
+  if (a->k.rows > 1 && (a->k.ld % per || a->v.ld % per)) return IDX_E_ALIGN;
+  return aligned(a->lse, 4) ? IDX_OK : IDX_E_ALIGN;
+}
+
+idx_status check_attn(const idx_attn *a) {
+  if (!a) return IDX_E_NULL;
+  const idx_status st = check_attn_arrays(a);
+  if (st) return st;
   if (a->L < 0 || a->n_sel < 0 || a->ld_sel < 0 || (a->q.T > 1 && a->ld_sel < a->n_sel)) return IDX_E_SHAPE;
   if (!a->slot_of_key && a->L > a->k.rows) return IDX_E_SHAPE;
   if (a->pool < 1 || a->pool > MAX_POOL || (a->pool & (a->pool - 1))) return IDX_E_UNSUPPORTED;
-  if ((int64_t)a->q.T * a->q.H >= (int64_t)1 << 26) return IDX_E_UNSUPPORTED;   // at most a wave each: 2^32 lanes
-  if (!std::isfinite(scale2_of(a))) return IDX_E_PARAM;
   if ((a->ks == nullptr) != (a->ke == nullptr) || (a->pool > 1 && !a->ks && a->q.T > 0)) return IDX_E_NULL;
   if (a->q.T > 0 && a->n_sel > 0 && !a->sel) return IDX_E_NULL;
-  // the attention kernel reads 16 bytes of a cache row at a time
-  const int64_t per = 128 / bits(a->k.fmt);
-  if (a->k.rows > 1 && (a->k.ld % per || a->v.ld % per)) return IDX_E_ALIGN;
-  if (!aligned(a->sel, 4) || !aligned(a->ks, 4) || !aligned(a->ke, 4) || !aligned(a->slot_of_key, 4) ||
-      !aligned(a->lse, 4))
+  if (!aligned(a->sel, 4) || !aligned(a->ks, 4) || !aligned(a->ke, 4) || !aligned(a->slot_of_key, 4))
     return IDX_E_ALIGN;
   return IDX_OK;
+}
+
+idx_status check_paged(const idx_paged *a) {
+  if (!a) return IDX_E_NULL;
+  const idx_status st = check_attn_arrays(a);
+  if (st) return st;
+  if (a->B < 0 || a->n_pages < 0 || a->ld_pages < 0 || a->ld_pages > MAX_LD || (a->B > 1 && a->ld_pages < a->n_pages))
+    return IDX_E_SHAPE;
+  if (a->B > MAX_REQUESTS) return IDX_E_UNSUPPORTED;
+  if (a->page < 1 || (a->page & (a->page - 1))) return IDX_E_UNSUPPORTED;
+  if ((int64_t)a->n_pages * a->page > INT32_MAX) return IDX_E_UNSUPPORTED;
+  if (a->window < 0 || a->first < 0) return IDX_E_PARAM;
+  if (a->q.T > 0 && a->B > 0 && (!a->cu_q || !a->len_k || (a->n_pages > 0 && !a->pages))) return IDX_E_NULL;
+  if (!aligned(a->pages, 4) || !aligned(a->cu_q, 4) || !aligned(a->len_k, 4)) return IDX_E_ALIGN;
+  return IDX_OK;
+}
+
+idx::PagedPlan plan_of(const idx_paged *a) {
+  return idx::plan_paged(a->q.T, a->B, a->k.H, a->q.H / a->k.H, a->q.D, a->k.fmt == IDX_K_FP8_E4M3,
+                         a->n_pages * a->page);
+}
+
+// Whether two row arrays that start together lie alike; true where they do not.
+bool alike(const idx_rows &a, const idx_rows &b) {
+  return a.data != b.data || (bits(a.dtype) == bits(b.dtype) && (a.T <= 1 || a.ld_t == b.ld_t) &&
+                              (a.H <= 1 || a.ld_h == b.ld_h));
+}
+bool same_sizes(const idx_rows &a, const idx_rows &b) { return a.T == b.T && a.H == b.H && a.D == b.D; }
+
+idx_status check_norm(const idx_norm *n) {
+  if (!n) return IDX_E_NULL;
+  idx_status st;
+  const idx_rows &x = n->x;
+  if ((st = check_rows(x, false, MAX_NORM))) return st;
+  if (!(n->eps >= 0.f) || !std::isfinite(n->eps)) return IDX_E_PARAM;
+  if (n->weight && (!value_type(n->weight_dtype))) return IDX_E_FORMAT;
+  if (!aligned(n->weight, 16)) return IDX_E_ALIGN;
+  if (x.T == 0 || x.H == 0) return IDX_OK;
+  if ((int64_t)x.T * x.H >= MAX_LANES / 64) return IDX_E_UNSUPPORTED;
+  if (!n->out.data && !n->to) return IDX_E_NULL;
+  if (n->residual.data) {
+    if ((st = check_rows(n->residual, false, MAX_NORM)) || (st = check_rows(n->total, true, MAX_NORM))) return st;
+    if (!same_sizes(x, n->residual) || !same_sizes(x, n->total)) return IDX_E_SHAPE;
+    if (n->residual.dtype != n->total.dtype) return IDX_E_FORMAT;
+    if (!alike(n->total, x) || !alike(n->total, n->residual)) return IDX_E_SHAPE;
+  }
+  if (n->out.data) {
+    if ((st = check_rows(n->out, true, MAX_NORM))) return st;
+    if (!same_sizes(x, n->out) || !alike(n->out, x)) return IDX_E_SHAPE;
+    if (n->residual.data && (n->out.data == n->total.data || !alike(n->out, n->residual))) return IDX_E_SHAPE;
+  }
+  if (n->to) {
+    const idx_cache &c = *n->to;
+    if ((st = check_cache(c, MAX_NORM))) return st;
+    if (c.fmt != IDX_K_FP8_E4M3) return IDX_E_UNSUPPORTED;
+    if (x.H == 1 ? (int64_t)c.H * c.D != x.D : c.H != x.H || c.D != x.D) return IDX_E_SHAPE;
+    if (c.rows < x.T) return IDX_E_SHAPE;
+    if (c.D != x.D && (c.D > MAX_GROUP || (c.D & (c.D - 1)))) return IDX_E_UNSUPPORTED;
+  }
+  return IDX_OK;
+}
+
+idx::NormRows norm_rows(const idx_rows &x) {
+  return {(uint8_t *)x.data, bytes_of(x.ld_t, x.dtype), bytes_of(x.ld_h, x.dtype), x.dtype};
 }
 
 idx::AttnPlan plan_of(const idx_attn *a) {
@@ -318,9 +394,89 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
   g.Hq = a->q.H;
   g.Hkv = a->k.H;
   g.G = a->q.H / a->k.H;
-  g.scale2 = scale2_of(a);
+  g.scale2 = scale2_of(a->scale);
   g.lse = a->lse;
   return launched(idx::launch_attn(g, a->q.dtype, a->k.fmt, a->q.D, plan, ws, (hipStream_t)stream));
+}
+
+idx_status idx_paged_attn_workspace(const idx_paged *a, size_t *bytes) {
+  if (!bytes) return IDX_E_NULL;
+  const idx_status st = check_paged(a);
+  if (st) return st;
+  *bytes = plan_of(a).bytes;
+  return IDX_OK;
+}
+
+idx_status idx_paged_attn(const idx_paged *a, void *ws, size_t ws_bytes, void *stream) {
+  idx_status st = check_paged(a);
+  if (st) return st;
+  if (a->q.T == 0 || a->B == 0) return IDX_OK;
+  const idx::PagedPlan plan = plan_of(a);
+  if (plan.bytes) {
+    if (!ws) return IDX_E_NULL;
+    if (ws_bytes < plan.bytes) return IDX_E_WORKSPACE;
+    if (!aligned(ws, 256)) return IDX_E_ALIGN;
+  }
+  idx::PagedArgs g{};
+  g.q = (const uint8_t *)a->q.data;
+  g.q_t = 2 * a->q.ld_t;
+  g.q_h = 2 * a->q.ld_h;
+  g.out = (uint8_t *)a->out.data;
+  g.out_t = 2 * a->out.ld_t;
+  g.out_h = 2 * a->out.ld_h;
+  g.k = (const uint8_t *)a->k.data;
+  g.v = (const uint8_t *)a->v.data;
+  g.row_bytes = (uint32_t)bytes_of(a->k.ld, a->k.fmt);
+  g.k_scale = (const float *)a->k.scale;
+  g.v_scale = (const float *)a->v.scale;
+  g.scale_row = a->k.ld_scale;
+  g.rows = a->k.rows;
+  g.pages = a->pages;
+  g.ld_pages = a->ld_pages;
+  while ((1 << g.page_sh) < a->page) ++g.page_sh;
+  g.max_len = a->n_pages * a->page;
+  g.cu_q = a->cu_q;
+  g.len_k = a->len_k;
+  g.B = a->B;
+  g.T = a->q.T;
+  g.Hq = a->q.H;
+  g.Hkv = a->k.H;
+  g.G = a->q.H / a->k.H;
+  g.window = a->window;
+  g.first = a->first;
+  g.scale2 = scale2_of(a->scale);
+  g.lse = a->lse;
+  if ((st = idx::debug_check_paged(g, stream))) return st;
+  return launched(idx::launch_paged(g, a->q.dtype, a->k.fmt, a->q.D, plan, ws, (hipStream_t)stream));
+}
+
+idx_status idx_rms_norm(const idx_norm *n, void *stream) {
+  const idx_status st = check_norm(n);
+  if (st) return st;
+  if (n->x.T == 0 || n->x.H == 0) return IDX_OK;
+  idx::NormJob j{};
+  j.x = norm_rows(n->x);
+  if (n->residual.data) {
+    j.residual = norm_rows(n->residual);
+    j.total = norm_rows(n->total);
+  }
+  if (n->out.data) j.out = norm_rows(n->out);
+  j.group = n->x.D;
+  if (n->to) {
+    j.codes = (uint8_t *)n->to->data;
+    j.codes_t = n->to->ld;
+    j.codes_h = n->to->D;
+    j.scale = (float *)n->to->scale;
+    j.scale_t = n->to->ld_scale;
+    j.group = n->to->D;
+  }
+  j.weight = (const uint8_t *)n->weight;
+  j.weight_dtype = n->weight_dtype;
+  j.T = n->x.T;
+  j.H = n->x.H;
+  j.D = n->x.D;
+  j.eps = n->eps;
+  return launched(idx::launch_norm(j, (hipStream_t)stream));
 }
 
 }  // extern "C"

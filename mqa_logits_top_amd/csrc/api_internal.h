@@ -35,6 +35,11 @@ idx_status debug_check(const int32_t *ks, const int32_t *ke, int32_t T, int32_t 
 // otherwise (slot nullable: nothing to check).
 idx_status debug_check_slots(const int32_t *slot, int32_t T, int64_t rows, void *stream);
 
+// In debug mode: check on the device the request bounds, lengths and pages of an attention over a paged cache
+// (launch_paged_check); as debug_check otherwise.
+struct PagedArgs;
+idx_status debug_check_paged(const PagedArgs &a, void *stream);
+
 // Launch timing (idx_launch_timing): timing_begin records a launch's first event on s when a
 // record is on, and returns a token for its slot (-1: not recorded); timing_end records the
 // second event (ok: the launch was enqueued) and the launch's description.

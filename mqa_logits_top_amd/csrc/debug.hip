@@ -17,6 +17,7 @@
 
 #include "../../include/idx.h"
 #include "api_internal.h"
+#include "paged.h"
 #include "rows.h"
 
 static __device__ uint32_t debug_word[1];
@@ -139,6 +140,16 @@ idx_status debug_check_slots(const int32_t *slot, int32_t T, int64_t rows, void 
   if (word_address(&word) != hipSuccess) return IDX_E_LAUNCH;
   hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, s, word);
   if (launch_slot_check(slot, T, rows, word, s) != hipSuccess) return IDX_E_LAUNCH;
+  return verdict(word, s);
+}
+
+idx_status debug_check_paged(const PagedArgs &a, void *stream) {
+  if (!debug_enabled()) return IDX_OK;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t *word = nullptr;
+  if (word_address(&word) != hipSuccess) return IDX_E_LAUNCH;
+  hipLaunchKernelGGL(clear_kernel, dim3(1), dim3(1), 0, s, word);
+  if (launch_paged_check(a, word, s) != hipSuccess) return IDX_E_LAUNCH;
   return verdict(word, s);
 }
 

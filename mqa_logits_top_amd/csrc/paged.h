@@ -1,0 +1,43 @@
+// Internal interface of the attention over a paged cache (paged.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/idx.h"
+
+namespace idx {
+
+struct PagedArgs {
+  const uint8_t *q;
+  int64_t q_t, q_h;          // bytes
+  uint8_t *out;
+  int64_t out_t, out_h;
+  const uint8_t *k, *v;
+  uint32_t row_bytes;        // of a slot, in both caches; a head is D values on
+  const float *k_scale, *v_scale;
+  int64_t scale_row;         // floats of a slot
+  int64_t rows;              // slots in both caches
+  const int32_t *pages;
+  int64_t ld_pages;
+  int32_t page_sh;           // log2 of the slots of a page
+  int32_t max_len;           // keys that a row of pages has room for
+  const int32_t *cu_q, *len_k;
+  int32_t B, T, Hq, Hkv, G;
+  int32_t window, first;
+  float scale2;              // scale * log2(e); launch_paged makes it > 0 ...
+  uint32_t q_sign, q_keep;   // ... and flips q's signs, or zeroes q, instead (filled there)
+  float *lse;
+};
+
+struct PagedPlan {
+  size_t bytes;              // workspace
+};
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len);
+hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
+                        hipStream_t s);
+
+// Debug check: cu_q ascending within [0, T], lengths within [0, max_len], the pages that some row sees a key of inside the
+// caches; else raises *word.
+hipError_t launch_paged_check(const PagedArgs &a, uint32_t *word, hipStream_t s);
+
+}  // namespace idx
