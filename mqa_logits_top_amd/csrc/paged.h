@@ -1,4 +1,4 @@
-// Internal interface of the attention over a paged cache (paged.hip).
+// Internal interface of the attention over a paged cache (paged.hip, paged_chunk.hip, paged_step.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -27,14 +27,30 @@ struct PagedArgs {
   float scale2;              // scale * log2(e); launch_paged makes it > 0 ...
   uint32_t q_sign, q_keep;   // ... and flips q's signs, or zeroes q, instead (filled there)
   float *lse;
+  // Filled by launch_paged from the plan
+  int32_t R;                 // tokens of a row tile
+  int32_t Gt, blocks;        // query heads of a row tile, and head blocks of a cache head
+  int32_t divide;            // whether keys may be divided over workgroups
+  int32_t slots, min_tiles;  // ... by aiming at this many workgroups, and at least this many key tiles for each
+  int32_t max_items;         // workgroups of the launch
+  float *part;               // divided items: [max_items][M][D] unnormalised out, then
+  float *part_ml;            // [max_items][M][2] reference, sum
 };
 
 struct PagedPlan {
+  bool chunk;                // paged_chunk.hip, else paged_step.hip
+  int32_t M;                 // rows (tokens x heads) of a workgroup
+  int32_t R, Gt, blocks;
+  int32_t divide, slots, min_tiles;
+  int64_t tiles;             // row tiles of the batch at most, times cache heads and head blocks
+  int64_t max_items;
   size_t bytes;              // workspace
 };
 PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len);
 hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
                         hipStream_t s);
+hipError_t launch_paged_chunk(const PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, hipStream_t s);
+hipError_t launch_paged_step(const PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, int32_t M, hipStream_t s);
 
 // Debug check: cu_q ascending within [0, T], lengths within [0, max_len], the pages that some row sees a key of inside the
 // caches; else raises *word.

@@ -1,86 +1,59 @@
-// Attention of new rows over every key, or a window of keys, of a paged cache.
-#include "paged.h"
-
+// Attention of new rows over every key, or a window of keys, of a paged cache: the division of the work, and the join of
+// keys that were divided.
 #include <cmath>
 
-#include "common.h"
+#include "attn_dev.h"
+#include "paged_dev.h"
 
 namespace idx {
 namespace {
 
-constexpr float NEG_INF = -__builtin_inff();
+constexpr int JOIN = 256;     // threads of a join
 
-__device__ __forceinline__ float value16(uint16_t u, bool bf16) {
-  return bf16 ? __uint_as_float((uint32_t)u << 16) : (float)__builtin_bit_cast(_Float16, u);
-}
-
-// The last request that starts at or before row t.
-__device__ __forceinline__ int request_of(const int32_t *cu, int B, int t) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
-// A product rounded by itself, never part of an fma: a score past 2^24 less its rounded maximum would be off otherwise.
-__device__ __forceinline__ float product(float x, float y) {
-#pragma clang fp contract(off)
-  return x * y;
-}
-
-// A wave serves one row and query head, a key at a time; a lane holds D / 64 dims.
-template <int D>
-__global__ __launch_bounds__(256) void paged_kernel(PagedArgs a, bool bf16, bool fp8) {
-  constexpr int N = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (item >= (int64_t)a.T * a.Hq) return;
-  const int t = (int)(item / a.Hq), h = (int)(item % a.Hq), kvh = h / a.G;
-  const int b = request_of(a.cu_q, a.B, t);
-  const int first_row = a.cu_q[b], n = a.cu_q[b + 1] - first_row;
-  if (t < first_row || t - first_row >= n) return;
-  const int64_t pos = (int64_t)min(max(a.len_k[b], 0), a.max_len) - n + (t - first_row);
-  const int64_t low = a.window && pos >= a.window ? pos - a.window + 1 : 0;
-  float q[N], o[N], ref = NEG_INF, sum = 0.f;
-  for (int i = 0; i < N; ++i) {
-    uint16_t u = *(const uint16_t *)(a.q + t * a.q_t + h * a.q_h + 2 * (lane * N + i));
-    u = (u & (uint16_t)a.q_keep) ^ (uint16_t)a.q_sign;
-    q[i] = value16(u, bf16);
-    o[i] = 0.f;
-  }
-  for (int64_t s = low > 0 && a.first > 0 ? 0 : low; s <= pos; ++s) {
-    if (s < low && s >= a.first) s = low;
-    const int64_t slot = ((int64_t)a.pages[b * a.ld_pages + (s >> a.page_sh)] << a.page_sh) + (s & ((1ll << a.page_sh) - 1));
-    if (slot < 0 || slot >= a.rows) continue;
-    float k[N], v[N];
-    for (int i = 0; i < N; ++i) {
-      const int e = kvh * D + lane * N + i;
-      if (fp8) {
-        k[i] = __builtin_amdgcn_cvt_f32_fp8((int)a.k[slot * a.row_bytes + e], 0) * a.k_scale[slot * a.scale_row + kvh];
-        v[i] = __builtin_amdgcn_cvt_f32_fp8((int)a.v[slot * a.row_bytes + e], 0) * a.v_scale[slot * a.scale_row + kvh];
-      } else {
-        k[i] = value16(*(const uint16_t *)(a.k + slot * a.row_bytes + 2 * e), bf16);
-        v[i] = value16(*(const uint16_t *)(a.v + slot * a.row_bytes + 2 * e), bf16);
-      }
+// Joins the parts of a row tile's rows, JOIN / (D / 4) rows at a time, D / 4 threads to one.
+template <bool BF16, int D, int KT, bool CHUNK>
+__global__ __launch_bounds__(JOIN) void join_kernel(PagedArgs a, int M, int slices) {
+  constexpr int QUADS = D / 4;
+  const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
+  const uint32_t member = blockIdx.x % mu, rest = blockIdx.x / mu;
+  const int slice = (int)(rest % (uint32_t)slices);
+  Item w;
+  if (!find_item<KT, CHUNK, true>(a, rest / (uint32_t)slices, w) || w.splits == 1) return;
+  const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
+  const int heads = min(a.Gt, a.G - hb * a.Gt), d = 4 * (threadIdx.x % QUADS);
+  for (int row = slice * (M / slices) + threadIdx.x / QUADS; row < (slice + 1) * (M / slices); row += JOIN / QUADS) {
+    const int tok = row / a.Gt, h = row - tok * a.Gt;
+    if (tok >= a.R || h >= heads || w.row0 + tok >= w.r.n) continue;
+    const int64_t at0 = ((int64_t)w.first_item * mu + member) * M + row, step = (int64_t)w.next * mu * M;
+    float top = NEG_INF;
+    for (int s = 0; s < w.splits; ++s) top = __builtin_fmaxf(top, a.part_ml[2 * (at0 + s * step)]);
+    const float ref = top == NEG_INF ? 0.f : top;
+    float total = 0.f;
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < w.splits; ++s) {
+      const int64_t at = at0 + s * step;
+      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
+      total += f * a.part_ml[2 * at + 1];
+      r += f * *(const f32x4 *)(a.part + at * D + d);
     }
-    float dot = 0.f;
-    for (int i = 0; i < N; ++i) dot = __builtin_fmaf(q[i], k[i], dot);
-    dot = product(wave_reduce_f32(dot, [](float x, float y) { return x + y; }), a.scale2);
-    const float to = __builtin_fmaxf(ref, dot);
-    const float f = to == ref ? 1.f : __builtin_amdgcn_exp2f(ref - to), p = dot == NEG_INF ? 0.f : __builtin_amdgcn_exp2f(dot - to);
-    sum = sum * f + p;
-    for (int i = 0; i < N; ++i) o[i] = o[i] * f + p * v[i];
-    ref = to;
+    r *= finish(total);
+    const int64_t t = w.r.from + w.row0 + tok, hq = kvh * a.G + hb * a.Gt + h;
+    *(uint2 *)(a.out + t * a.out_t + hq * a.out_h + 2 * d) =
+        make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
+    if (d == 0 && a.lse) a.lse[t * a.Hq + hq] = lse_of(top, total);
   }
-  const float f = sum == 0.f ? 0.f : 1.f / sum;
-  for (int i = 0; i < N; ++i) {
-    const float x = o[i] * f;
-    *(uint16_t *)(a.out + t * a.out_t + h * a.out_h + 2 * (lane * N + i)) =
-        bf16 ? __builtin_bit_cast(uint16_t, (__bf16)x) : __builtin_bit_cast(uint16_t, (_Float16)x);
-  }
-  if (lane == 0 && a.lse) a.lse[item] = sum == 0.f ? NEG_INF : 0.69314718055994531f * (ref + __builtin_amdgcn_logf(sum));
+}
+
+template <bool BF16, int D>
+hipError_t launch_join(const PagedArgs &a, const PagedPlan &plan, hipStream_t s) {
+  const int slices = plan.M >= 32 ? plan.M / 32 : 1;
+  const dim3 grid((unsigned)(plan.tiles * slices));
+  if (plan.chunk)
+    hipLaunchKernelGGL((join_kernel<BF16, D, 64, true>), grid, dim3(JOIN), 0, s, a, plan.M, slices);
+  else
+    hipLaunchKernelGGL((join_kernel<BF16, D, 32, false>), grid, dim3(JOIN), 0, s, a, plan.M, slices);
+  return hipGetLastError();
 }
 
 __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
@@ -104,24 +77,54 @@ __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
 
 }  // namespace
 
-PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len) { return {}; }
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len) {
+  PagedPlan p{};
+  const int32_t live = B < T ? (B > 0 ? B : 1) : (T > 0 ? T : 1);   // requests that can have rows
+  p.chunk = true;
+  p.M = 256;
+  p.Gt = G < p.M ? G : p.M;
+  p.blocks = (G + p.Gt - 1) / p.Gt;
+  p.R = p.M / p.Gt;
+  const int64_t mu = (int64_t)Hkv * p.blocks;
+  const int32_t kt = p.chunk ? 64 : 32;
+  p.slots = p.chunk ? (D == 64 ? 512 : 256) : 1024;
+  p.min_tiles = 8;
+  const int64_t divided = (T / p.R + live) * mu;      // row tiles at most
+  p.divide = divided < 3 * p.slots && max_len > 2 * p.min_tiles * kt && B <= 4096;
+  if (p.divide) {
+    p.tiles = divided;
+    p.max_items = divided + p.slots + p.slots / 8 + mu;
+    p.bytes = ((size_t)p.max_items * p.M * (D + 2) * 4 + 255) / 256 * 256;
+  } else {
+    p.tiles = (T / p.R + (int64_t)B) * mu;            // the numbers that tiles are looked up by
+    p.max_items = p.tiles;
+  }
+  return p;
+}
 
 hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
                         hipStream_t s) {
-  const int64_t items = (int64_t)a.T * a.Hq;
-  if (items <= 0) return hipSuccess;
+  if (plan.max_items <= 0) return hipSuccess;
+  if (plan.max_items > INT32_MAX / 32) return hipErrorInvalidValue;
+  if (a.rows == 0) a.max_len = 0;   // no slot that could be read
   // a negative factor turns q over instead, so that the largest product comes from the largest dot
   a.q_sign = a.scale2 < 0.f ? 0x80008000u : 0u;
   // and a factor of zero zeroes q, so that the product of the mask's -inf with it stays -inf
   a.q_keep = a.scale2 == 0.f ? 0u : ~0u;
   a.scale2 = a.scale2 == 0.f ? 1.f : std::fabs(a.scale2);
-  const dim3 grid((unsigned)((items + 3) / 4));
-  const bool bf16 = dtype == IDX_K_BF16, fp8 = fmt == IDX_K_FP8_E4M3;
-  if (D == 64)
-    hipLaunchKernelGGL(paged_kernel<64>, grid, dim3(256), 0, s, a, bf16, fp8);
-  else
-    hipLaunchKernelGGL(paged_kernel<128>, grid, dim3(256), 0, s, a, bf16, fp8);
-  return hipGetLastError();
+  a.R = plan.R;
+  a.Gt = plan.Gt;
+  a.blocks = plan.blocks;
+  a.divide = plan.divide;
+  a.slots = plan.slots;
+  a.min_tiles = plan.min_tiles;
+  a.max_items = (int32_t)plan.max_items;
+  a.part = (float *)ws;
+  a.part_ml = a.part + (size_t)plan.max_items * plan.M * D;
+  const hipError_t e = launch_paged_chunk(a, dtype, fmt, D, s);
+  if (e != hipSuccess || !plan.divide) return e;
+  if (D == 64) return dtype == IDX_K_BF16 ? launch_join<true, 64>(a, plan, s) : launch_join<false, 64>(a, plan, s);
+  return dtype == IDX_K_BF16 ? launch_join<true, 128>(a, plan, s) : launch_join<false, 128>(a, plan, s);
 }
 
 hipError_t launch_paged_check(const PagedArgs &a, uint32_t *word, hipStream_t s) {

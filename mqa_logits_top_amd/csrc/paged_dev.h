@@ -1,0 +1,172 @@
+// How the workgroups of an attention over a paged cache find their rows and keys (paged_chunk.hip, paged_step.hip and the
+// join in paged.hip).
+//
+// A request's rows are taken R tokens at a time, each with Gt query heads of one cache head: a row tile of up to M rows.
+// Its keys are tiles of KT, in the order first keys, window (one run without a window).  Where the row tiles are too few to
+// fill the machine, the tiles of a row tile's keys are divided over several workgroups, whose results a second kernel
+// joins.  Lengths are known on the device only, so every workgroup works the division out for itself, from all of them,
+// and finds its own item by a prefix sum over the requests: the items come out equal whatever the lengths are, and a
+// captured launch takes new ones.  64 requests cost a workgroup about 1 us.  Undivided launches find their request by a
+// search in cu_q instead.
+#pragma once
+#include "common.h"
+#include "paged.h"
+
+namespace idx {
+
+struct Request {
+  int32_t from, n, len;   // rows [from, from + n), the last of len keys
+};
+__device__ __forceinline__ Request request(const PagedArgs &a, int b) {
+  Request r;
+  r.from = min(max(a.cu_q[b], 0), a.T);
+  r.n = min(max(a.cu_q[b + 1], r.from), a.T) - r.from;
+  r.len = min(max(a.len_k[b], 0), a.max_len);
+  return r;
+}
+
+// Key tiles of the rows row0 .. row0 + R - 1 of a request.
+struct KeyTiles {
+  int32_t hi;      // one past the last key that a row sees
+  int32_t firsts;  // tiles of first keys, from key 0
+  int32_t base;    // key at which the tile after them starts
+  int32_t count;
+};
+template <int KT>
+__device__ __forceinline__ KeyTiles key_tiles(const PagedArgs &a, const Request &r, int32_t row0, int32_t R) {
+  KeyTiles k{0, 0, 0, 0};
+  const int32_t p0 = r.len - r.n + row0, p1 = r.len - r.n + min(row0 + R, r.n) - 1;
+  if (p1 < 0) return k;
+  k.hi = p1 + 1;
+  const int64_t low = a.window ? (int64_t)p0 - a.window + 1 : 0;
+  const int32_t lo = low > 0 ? (int32_t)(low / KT) : 0;   // tile of the first row's window
+  k.firsts = (int32_t)(((int64_t)min((int64_t)a.first, (int64_t)lo * KT) + KT - 1) / KT);
+  k.base = lo * KT;
+  k.count = k.firsts + (k.hi + KT - 1) / KT - lo;
+  return k;
+}
+
+struct Item {
+  Request r;
+  int32_t b;
+  int32_t row0;            // first row of the tile, within the request
+  int32_t split, splits;
+  int32_t first_item;      // of the tile's split 0
+  int32_t next;            // items from one split of a tile to the next
+};
+
+__device__ __forceinline__ int32_t wave_sum_i(int32_t x) { return (int32_t)wave_sum((uint32_t)x); }
+
+// The id-th item (or, with TILES, the id-th row tile) of the launch's list; false: there is none.  Every lane of the wave
+// calls it with the same id and gets the same answer.
+template <int KT, bool CHUNK, bool TILES>
+__device__ bool find_item(const PagedArgs &a, uint32_t id, Item &w) {
+  const int lane = threadIdx.x & 63;
+  const int32_t R = a.R;
+  w.split = 0;
+  w.splits = 1;
+  w.first_item = (int32_t)id;
+  w.next = 0;
+  if (!a.divide) {
+    // request b's tiles are numbered from cu_q[b] / R + b on: that is at least as many numbers as it has tiles
+    int lo = 0, count = a.B;
+    while (count > 1) {
+      const int step = (count + 63) / 64, at = lane * step;
+      const bool ok = at < count && (uint32_t)(min(max(a.cu_q[lo + at], 0), a.T) / R + lo + at) <= id;
+      const uint64_t m = __ballot(ok);
+      const int k = m ? 63 - __builtin_clzll(m) : 0;
+      lo += k * step;
+      count = min(step, count - k * step);
+    }
+    w.b = lo;
+    w.r = request(a, lo);
+    const int64_t t = (int64_t)id - (w.r.from / R + lo);
+    if (t < 0 || t * R >= w.r.n) return false;
+    // the last rows, which see the most keys, first
+    const int32_t nt = (w.r.n + R - 1) / R;
+    w.row0 = (nt - 1 - (int32_t)t) * R;
+    return true;
+  }
+  // what the launch has to do, in key tiles
+  const int32_t mu = a.Hkv * a.blocks;
+  float total = 0.f;   // of the launch's list, as the division needs it: no more exact than it is
+  int32_t most = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    int32_t nt = 0, c = 0;
+    if (b0 + lane < a.B) {
+      const Request r = request(a, b0 + lane);
+      nt = (r.n + R - 1) / R;
+      c = nt ? key_tiles<KT>(a, r, (nt - 1) * R, R).count : 0;
+    }
+    total += wave_reduce_f32((float)nt * (float)c, [](float x, float y) { return x + y; });
+    most = max(most, (int32_t)wave_max((uint32_t)c));
+  }
+  const float share = total * (float)mu / (float)a.slots;
+  int32_t chunk = max((int32_t)__builtin_fminf(share, 0x1p30f) + 1, a.min_tiles);
+  if constexpr (CHUNK) {
+    // Few and long items: the longest list in 1 to 8 parts, whichever would be through first.  Equal items run in rounds of
+    // `slots`; unequal ones end within one item of an even share.  A divided item costs its partial output and the join,
+    // about 8 tiles' time.
+    int64_t best = (int64_t)1 << 62;
+    chunk = max(most, 1);
+    for (int s = 1; s <= 8; ++s) {
+      const int32_t size = (most + s - 1) / s;
+      if (s > 1 && size < a.min_tiles) break;
+      int32_t items = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int32_t n = 0;
+        if (b0 + lane < a.B) {
+          const Request r = request(a, b0 + lane);
+          const int32_t nt = (r.n + R - 1) / R;
+          if (nt) n = nt * max((key_tiles<KT>(a, r, (nt - 1) * R, R).count + size - 1) / max(size, 1), 1);
+        }
+        items += wave_sum_i(n);
+      }
+      if (s > 1 && (int64_t)items * mu > a.max_items) break;
+      const int64_t rounds = ((int64_t)items * mu + a.slots - 1) / a.slots;
+      const int64_t even = rounds * size, uneven = (int64_t)share + size;
+      const int64_t t = min(even, uneven) + (s > 1 ? 8 * rounds : 0);
+      if (t < best) {
+        best = t;
+        chunk = max(size, 1);
+      }
+    }
+  }
+  int32_t items = 0, tiles = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    int32_t nt = 0, ns = 1;
+    if (b0 + lane < a.B) {
+      const Request r = request(a, b0 + lane);
+      nt = (r.n + R - 1) / R;
+      if (nt) ns = max((key_tiles<KT>(a, r, (nt - 1) * R, R).count + chunk - 1) / chunk, 1);
+    }
+    const int32_t mine = TILES ? nt : nt * ns;
+    const int32_t upto = (int32_t)wave_incl_scan((uint32_t)mine), here = TILES ? tiles : items;
+    const uint64_t m = __ballot((int64_t)id < (int64_t)here + upto);
+    if (m) {
+      const int k = __builtin_ctzll(m);
+      const int32_t n = __builtin_amdgcn_readlane(nt, k), s = __builtin_amdgcn_readlane(ns, k);
+      const int32_t at = (int32_t)id - here - (__builtin_amdgcn_readlane(upto, k) - __builtin_amdgcn_readlane(mine, k));
+      const int32_t before = items + (TILES ? __builtin_amdgcn_readlane((int32_t)wave_incl_scan((uint32_t)(nt * ns)), k) - n * s
+                                            : __builtin_amdgcn_readlane(upto, k) - n * s);
+      w.b = b0 + k;
+      w.r = request(a, w.b);
+      w.splits = s;
+      w.split = TILES ? 0 : at / n;
+      const int32_t tile = TILES ? at : at % n;
+      w.row0 = (n - 1 - tile) * R;
+      w.first_item = before + tile;
+      w.next = n;
+      return true;
+    }
+    if constexpr (TILES) {
+      tiles += __builtin_amdgcn_readlane(upto, 63);
+      items += wave_sum_i(nt * ns);
+    } else {
+      items += __builtin_amdgcn_readlane(upto, 63);
+    }
+  }
+  return false;
+}
+
+}  // namespace idx
