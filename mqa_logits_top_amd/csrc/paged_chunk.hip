@@ -1,5 +1,6 @@
 // Attention over a paged cache for requests of many rows: 64 rows (tokens x heads of one cache head) to a wave, four waves
 // to a workgroup, which share tiles of 64 keys in LDS.
+#include <array>
 #include <cmath>
 #include <type_traits>
 
@@ -15,6 +16,8 @@ constexpr int KT = 64;        // keys of a tile
 constexpr int WAVES = 4;
 constexpr int M = 64 * WAVES; // rows of a workgroup
 constexpr int KSTAGES = 4, VSTAGES = 3, IDS = 8;
+
+#define INLINE __attribute__((always_inline))
 
 template <bool BF16>
 __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
@@ -42,7 +45,9 @@ constexpr int chunk_lds() {
   return (KSTAGES + VSTAGES) * KT * (FP8 ? D : 2 * D) + WAVES * IDS * KT * 4 + (FP8 ? KSTAGES * WAVES * 256 : 0);
 }
 
-template <bool BF16, bool FP8, int D>
+// RUNS: pages of 16 slots and more, and a cache of whole pages: the 16 keys of a tile that a wave brings follow each other
+// in a cache, and their copies have one scalar address.
+template <bool BF16, bool FP8, int D, bool RUNS>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(PagedArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
   constexpr bool TWO = FP8 && !BF16;      // ... and, for fp16 results, two parts
@@ -67,6 +72,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   Item w;
   if (!find_item<KT, true, false>(a, blockIdx.x / mu, w)) return;
+  w = uniform(w);
   const int head0 = kvh * a.G + hb * a.Gt, heads = min(a.Gt, a.G - hb * a.Gt);
   const KeyTiles kt = key_tiles<KT>(a, w.r, w.row0, a.R);
   const int v0 = (int)((int64_t)kt.count * w.split / w.splits), v1 = (int)((int64_t)kt.count * (w.split + 1) / w.splits);
@@ -93,8 +99,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       max_lb = max(max_lb, lb[m]);
     }
   }
-  min_pos = (int32_t)wave_min((uint32_t)min_pos ^ 0x80000000u) ^ 0x80000000u;
-  max_lb = (int32_t)(wave_max((uint32_t)(max_lb + 1)) - 1u);
+  min_pos = __builtin_amdgcn_readfirstlane((int)(wave_min((uint32_t)min_pos ^ 0x80000000u) ^ 0x80000000u));
+  max_lb = __builtin_amdgcn_readfirstlane((int)(wave_max((uint32_t)(max_lb + 1)) - 1u));
   const bool any_row = __any(real[0] || real[1]);
 
   // ---- copies
@@ -102,44 +108,67 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   uint32_t *const ids = (uint32_t *)(lds + IDS_AT) + wave * IDS * KT;
   const uint32_t page_mask = (1u << a.page_sh) - 1u, rows = (uint32_t)a.rows, max_page = (rows - 1u) >> a.page_sh;
   const int32_t last_key = kt.hi - 1;
-  auto key0 = [&](int v) {    // of the split's v-th tile; behind its last one, that one
+  auto key0 = [&](int v) INLINE {    // of the split's v-th tile; behind its last one, that one
     const int x = v0 + min(v, nv - 1);
     return x < kt.firsts ? x * KT : kt.base + (x - kt.firsts) * KT;
   };
-  auto request_ids = [&](int v) {
+  auto request_ids = [&](int v) INLINE {
     const int32_t key = min(key0(v) + lane, last_key);
     copy4((const float *)(table + (key >> a.page_sh)), lds_addr(ids + (v & (IDS - 1)) * KT));
   };
   // slot of a key, from its page's id; a page outside the cache gives slot 0 and does not count
-  auto slot_of = [&](uint32_t id, int32_t key, bool &ok) -> uint32_t {
+  auto slot_of = [&](uint32_t id, int32_t key, bool &ok) INLINE -> uint32_t {
     const uint32_t s = (id << a.page_sh) + ((uint32_t)key & page_mask);
     ok = id <= max_page && s < rows;
     return ok ? s : 0u;
   };
   const int my_row = lane / CH;   // of a copy
-  auto swizzle_k = [](int r) { return (r / PER) & (CH - 1); };
-  auto swizzle_v = [](int r) {
+  auto swizzle_k = [](int r) INLINE { return (r / PER) & (CH - 1); };
+  auto swizzle_v = [](int r) INLINE {
     if constexpr (FP8) return D == 128 ? (((r >> 1) & 1) << 1) | (((r >> 3) & 1) << 2) : ((r >> 3) & 1) << 1;
     return D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
   };
   const uint8_t *kbase = a.k + (int64_t)RB * kvh, *vbase = a.v + (int64_t)RB * kvh;
-  auto row_slot = [&](int v, int u) {
-    const int r = 16 * wave + u * RPC + my_row;
+  // The wave's 16 rows of a tile: their slots, or with RUNS the byte offset of the first, the lanes' being a constant on.
+  using Slots = std::conditional_t<RUNS, uint64_t, std::array<uint32_t, NI>>;
+  auto slots_of = [&](int v) INLINE -> Slots {
+    const uint32_t *p = ids + (v & (IDS - 1)) * KT + 16 * wave;
+    const int32_t k0 = key0(v) + 16 * wave;
     bool ok;
-    return slot_of(ids[(v & (IDS - 1)) * KT + r], min(key0(v) + r, last_key), ok);
+    if constexpr (RUNS) {
+      const uint32_t id = (uint32_t)__builtin_amdgcn_readfirstlane((int)p[0]);
+      return (uint64_t)slot_of(id, min(k0, last_key) & ~15, ok) * a.row_bytes;
+    } else {
+      Slots s;
+#pragma unroll
+      for (int u = 0; u < NI; ++u) {
+        const int r = u * RPC + my_row;
+        s[u] = slot_of(p[r], min(k0 + r, last_key), ok);
+      }
+      return s;
+    }
   };
-  auto request_k = [&](int v, int stage, int u) {
-    const int r = 16 * wave + u * RPC + my_row;
-    copy16(kbase, (uint64_t)row_slot(v, u) * a.row_bytes + ((((lane & (CH - 1)) ^ swizzle_k(r))) << 4),
-           lds_addr(lds + stage * KV + (16 * wave + u * RPC) * RB));
+  uint32_t k_off[NI], v_off[NI];   // of the lane's chunk: with RUNS also of its row
+#pragma unroll
+  for (int u = 0; u < NI; ++u) {
+    const int r = u * RPC + my_row;
+    k_off[u] = (uint32_t)(((lane & (CH - 1)) ^ swizzle_k(r)) << 4) + (RUNS ? (uint32_t)r * a.row_bytes : 0u);
+    v_off[u] = (uint32_t)(((lane & (CH - 1)) ^ swizzle_v(r)) << 4) + (RUNS ? (uint32_t)r * a.row_bytes : 0u);
+  }
+  auto request = [&](const uint8_t *base, const Slots &s, uint32_t off, int u, uint32_t at) INLINE {
+    if constexpr (RUNS)
+      copy16(uniform(base + s), off, at);
+    else
+      copy16(base, (uint64_t)s[u] * a.row_bytes + off, at);
   };
-  auto request_v = [&](int v, int stage, int u) {
-    const int r = 16 * wave + u * RPC + my_row;
-    copy16(vbase, (uint64_t)row_slot(v, u) * a.row_bytes + ((((lane & (CH - 1)) ^ swizzle_v(r))) << 4),
-           lds_addr(lds + V_AT + stage * KV + (16 * wave + u * RPC) * RB));
+  auto request_k = [&](int stage, const Slots &s, int u) INLINE {
+    request(kbase, s, k_off[u], u, lds_addr(lds + stage * KV + (16 * wave + u * RPC) * RB));
+  };
+  auto request_v = [&](int stage, const Slots &s, int u) INLINE {
+    request(vbase, s, v_off[u], u, lds_addr(lds + V_AT + stage * KV + (16 * wave + u * RPC) * RB));
   };
   // lanes 0 .. 15 bring the wave's keys' scales, 16 .. 31 their values', the others the same again
-  auto request_scales = [&](int v) {
+  auto request_scales = [&](int v) INLINE {
     if constexpr (FP8) {
       const int r = 16 * wave + (lane & 15);
       bool ok;
@@ -156,40 +185,47 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
 #pragma unroll
     for (int d = 0; d < DN; ++d) o[m][d] = f32x16{};
 
+  Slots ks, vs;       // of K(j + 3) and V(j + 2) in step j
   if (nv > 0) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i) request_ids(i);
+    for (int i = 0; i < 6; ++i) request_ids(i);
     copies_left<0>();
+    const Slots s0 = slots_of(0), s1 = slots_of(1);
+    vs = slots_of(2);
+    ks = slots_of(3);
     request_scales(0);
 #pragma unroll
-    for (int u = 0; u < NI; ++u) request_k(0, 0, u);
+    for (int u = 0; u < NI; ++u) request_k(0, s0, u);
     request_scales(1);
 #pragma unroll
-    for (int u = 0; u < NI; ++u) request_k(1, 1, u);
+    for (int u = 0; u < NI; ++u) request_k(1, s1, u);
 #pragma unroll
-    for (int u = 0; u < NI; ++u) request_v(0, 0, u);
+    for (int u = 0; u < NI; ++u) request_v(0, s0, u);
     // as many as a step has
     request_scales(2);
 #pragma unroll
-    for (int u = 0; u < NI; ++u) request_k(2, 2, u);
+    for (int u = 0; u < NI; ++u) request_k(2, vs, u);
 #pragma unroll
-    for (int u = 0; u < NI; ++u) request_v(1, 1, u);
-    request_ids(4);
+    for (int u = 0; u < NI; ++u) request_v(1, s1, u);
+    request_ids(5);
   }
-  auto meet = [&] {   // all but the last step's copies are there, the other waves' too
+  auto meet = [&]() INLINE {   // all but the last step's copies are there, the other waves' too
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NSTEP) : "memory");
   };
-  int vs = 0;         // stage of V(j)
+  int vst = 0;        // stage of V(j)
   if (!any_row) {
     // no row of its own: the wave's share of the copies only
     for (int j = 0; j < nv; ++j) {
       meet();
-      const int vn = vs == 0 ? 2 : vs - 1;
       request_scales(j + 3);
-      for (int u = 0; u < NI; ++u) request_k(j + 3, (j + 3) & (KSTAGES - 1), u);
-      for (int u = 0; u < NI; ++u) request_v(j + 2, vn, u);
-      request_ids(j + 5);
-      vs = vs == 2 ? 0 : vs + 1;
+#pragma unroll
+      for (int u = 0; u < NI; ++u) request_k((j + 3) & (KSTAGES - 1), ks, u);
+#pragma unroll
+      for (int u = 0; u < NI; ++u) request_v(vst == 0 ? 2 : vst - 1, vs, u);
+      request_ids(j + 6);
+      vs = ks;
+      ks = slots_of(j + 4);
+      vst = vst == 2 ? 0 : vst + 1;
     }
   } else if (nv > 0) {
     // Q^T as B operands: lane l holds row l % 32 and 8 dims of each 16
@@ -202,6 +238,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         u32x4 x = {0u, 0u, 0u, 0u};
         if (real[m]) x = *(const u32x4 *)(a.q + q_at[m] + 2 * e);
         q[m][s] = (x & a.q_keep) ^ a.q_sign;
+        // with 128 dims the queries' place is the accumulation registers, which the products read as well
+        if constexpr (D == 128) asm volatile("" : "+a"(q[m][s]));
       }
     const uint32_t k_row = (uint32_t)(c * RB), k_sw = (uint32_t)swizzle_k(c);
     // V^T: lane 4 r + x of a group points to key r, dims 4 x (E4M3: lane 2 r + x, dims 8 x)
@@ -215,38 +253,29 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     float sc[2] = {a.scale2, a.scale2}, nb[2] = {0.f, 0.f};
     bool big = false, masked = false;
 
-    auto load_k = [&](const uint8_t *kp, int g) {
+    auto load_k = [&](const uint8_t *kp, int g) INLINE {
       return *(const u32x4 *)(kp + k_row + (((uint32_t)(2 * g + hl) ^ k_sw) << 4));
     };
     // scores of 32 keys: S^T = K Q^T
     f32x16 sa[2], sb[2];
-    auto k_scales = [&](int v, int half, f32x16 *s) {
-      if constexpr (FP8) {
-        const float *p = (const float *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 32 * half + 8 * x + 4 * hl;
-          const f32x4 f = *(const f32x4 *)(p + (key >> 4) * 64 + (key & 15));
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            s[0][4 * x + j] *= f[j];
-            s[1][4 * x + j] *= f[j];
-          }
-        }
-      }
+    auto scales_at = [&](int v, int half, int x, int value) INLINE {   // of keys 32 half + 8 x + 4 (l / 32) .. + 3
+      const float *p = (const float *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256) + 16 * value;
+      const int key = 32 * half + 8 * x + 4 * hl;
+      return *(const f32x4 *)(p + (key >> 4) * 64 + (key & 15));
     };
-    // which of the 32 keys from k0 on, half a tile, have a slot
-    auto good_keys = [&](int v, int half) -> uint32_t {
+    // which keys of a tile have a slot
+    auto good_keys = [&](int v) INLINE -> uint64_t {
+      const uint32_t id = ids[(v & (IDS - 1)) * KT + lane];
+      if constexpr (RUNS) return __ballot(id <= max_page);
       bool ok;
-      const int r = 32 * half + c;
-      slot_of(ids[(v & (IDS - 1)) * KT + r], min(key0(v) + r, last_key), ok);
-      return (uint32_t)__ballot(ok);
+      slot_of(id, min(key0(v) + lane, last_key), ok);
+      return __ballot(ok);
     };
-    auto mask = [&](int v, int half, f32x16 *s) -> bool {
-      const int32_t k0 = key0(v) + 32 * half;
-      const uint32_t good = good_keys(v, half);
-      const bool whole = k0 + 31 <= min_pos && (k0 > max_lb || k0 + 31 < a.first) && good == ~0u;
-      if (whole) return false;
+    // 32 keys from k0 on: every row sees them all if k0 is one of these, and the slots are good
+    const uint32_t whole0 = min_pos - 31 > max_lb ? (uint32_t)max_lb + 1u : ~0u;
+    const uint32_t whole_span = min_pos - 31 > max_lb ? (uint32_t)(min_pos - 31 - max_lb - 1) : 0u;
+    auto mask = [&](int32_t k0, uint32_t good, f32x16 *s) INLINE -> bool {
+      if ((uint32_t)k0 - whole0 <= whole_span && good == ~0u) return false;
       asm volatile("");   // stays a branch
       const uint32_t mine = good >> (4 * hl);
 #pragma unroll
@@ -261,22 +290,27 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       }
       return true;
     };
-    auto settle = [&](f32x16 *s, const float *top) {
-      // The reference moves only when a score is 2^8 above it (LIFT lower than the largest): see attn.hip
-      if (__any(top[0] * a.scale2 > ref[0] + (8.f + LIFT) || top[1] * a.scale2 > ref[1] + (8.f + LIFT))) {
+    // The reference moves only when a score is 2^8 above it (LIFT lower than the largest): the accumulators are rescaled
+    // a few times a row instead of at most tiles.  Each row by its own scores, so that its bits do not depend on its
+    // neighbours'.
+    float high[2] = {NEG_INF, NEG_INF};   // scores, before their scale, from which on it moves
+    auto settle = [&](f32x16 *s, const float *top) INLINE {
+      if (__any(top[0] > high[0] || top[1] > high[1])) {
         bool far = false;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          // each row by its own scores, so that its bits do not depend on its neighbours'
-          const float high = pair_max(top[m] * a.scale2);
-          const float to = high > ref[m] + (8.f + LIFT) ? high - LIFT : ref[m];
+          const float both = pair_max(top[m]);
+          const float to = both > high[m] ? __builtin_fmaxf(ref[m], product(both, a.scale2) - LIFT) : ref[m];
           const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
           sum[m] *= f;
 #pragma unroll
           for (int d = 0; d < DN; ++d) o[m][d] *= f;
           ref[m] = to;
+          const bool rounds = __builtin_fabsf(to) >= BIG && to != NEG_INF;   // then every tile is looked at
+          high[m] = rounds ? NEG_INF : (to + (8.f + LIFT)) / a.scale2;
+          sc[m] = a.scale2;
           nb[m] = to == NEG_INF ? 0.f : -to;
-          far |= __builtin_fabsf(to) >= BIG && to != NEG_INF;
+          far |= rounds;
         }
         big = __any(far);
       }
@@ -293,7 +327,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         }
       }
     };
-    auto first_max = [&](const f32x16 *s, float *top) {
+    auto first_max = [&](const f32x16 *s, float *top) INLINE {
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         top[m] = s[m][0];
@@ -301,29 +335,24 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         for (int i = 1; i < 16; ++i) top[m] = __builtin_fmaxf(top[m], s[m][i]);
       }
     };
-    auto qk = [&](const uint8_t *kp, f32x16 *s) {
-      s[0] = f32x16{};
-      s[1] = f32x16{};
-      static_for<NKL>([&](auto gc) {
-        constexpr int g = decltype(gc)::value;
-        const u32x4 x = load_k(kp, g);
-        if constexpr (FP8) {
-          const u32x4 lo = {codes2<BF16, false>(x.x), codes2<BF16, true>(x.x), codes2<BF16, false>(x.y),
-                            codes2<BF16, true>(x.y)};
-          const u32x4 hi = {codes2<BF16, false>(x.z), codes2<BF16, true>(x.z), codes2<BF16, false>(x.w),
-                            codes2<BF16, true>(x.w)};
+    // One load's share of S^T += K Q^T
+    auto qk = [&](auto gc, u32x4 x, f32x16 *s) INLINE {
+      constexpr int g = decltype(gc)::value;
+      if constexpr (g == 0) s[0] = s[1] = f32x16{};
+      if constexpr (FP8) {
+        const u32x4 lo = {codes2<BF16, false>(x.x), codes2<BF16, true>(x.x), codes2<BF16, false>(x.y), codes2<BF16, true>(x.y)};
+        const u32x4 hi = {codes2<BF16, false>(x.z), codes2<BF16, true>(x.z), codes2<BF16, false>(x.w), codes2<BF16, true>(x.w)};
 #pragma unroll
-          for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(lo, q[m][2 * g], s[m]);
+        for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(lo, q[m][2 * g], s[m]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(hi, q[m][2 * g + 1], s[m]);
-        } else {
+        for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(hi, q[m][2 * g + 1], s[m]);
+      } else {
 #pragma unroll
-          for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(x, q[m][g], s[m]);
-        }
-      });
+        for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(x, q[m][g], s[m]);
+      }
     };
     // V^T of dims 32 d .. and the 16 keys from 16 u on
-    auto load_v = [&](const uint8_t *vp, int u, int d) -> u32x4 {
+    auto load_v = [&](const uint8_t *vp, int u, int d) INLINE -> u32x4 {
       if constexpr (FP8) {
         const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
             (__attribute__((address_space(3))) i32x2 *)(vp + 16 * u * RB + v_row + (((uint32_t)(2 * d) + v_ch) ^ v_sw) * 16));
@@ -341,49 +370,36 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         return r;
       }
     };
-    auto weights = [&](int v, int half, f32x16 *s, u32x4 (*p)[2], u32x4 (*rest)[2]) {
-      f32x4 vsc[4];
+    u32x4 p[2][2], rest[2][2];   // weights of 16 keys each, and their second parts
+    f32x4 vsc[4];
+    // Weights of two keys, the n-th pair of the 16: keys in the order of the second product's steps
+    auto weigh = [&](int n, const f32x16 *s) INLINE {
+      const int m = n & 1, i = n >> 1 << 1;
+      float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i], sc[m], nb[m]));
+      float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i + 1], sc[m], nb[m]));
+      sum[m] += x;
+      sum[m] += y;
       if constexpr (FP8) {
-        const float *f = (const float *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256) + 16;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = 32 * half + 8 * x + 4 * hl;
-          vsc[x] = *(const f32x4 *)(f + (key >> 4) * 64 + (key & 15));
-        }
-        if (masked) {   // scales that are not finite reach the rows that see their keys through add_odd
-          asm volatile("");
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) vsc[x][j] = vsc[x][j] - vsc[x][j] == 0.f ? vsc[x][j] : 0.f;
-        }
+        x *= vsc[i / 4][i % 4];
+        y *= vsc[i / 4][i % 4 + 1];
       }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i], sc[m], nb[m]));
-          float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i + 1], sc[m], nb[m]));
-          sum[m] += x + y;
-          if constexpr (FP8) {
-            x *= vsc[i / 4][i % 4];
-            y *= vsc[i / 4][i % 4 + 1];
-          }
-          const uint32_t b = pack2<PV_BF16>(x, y);
-          p[m][i / 8][i % 8 / 2] = b;
-          if constexpr (TWO)
-            rest[m][i / 8][i % 8 / 2] =
-                pack2<true>(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xFFFF0000u));
-        }
+      uint32_t b = pack2<PV_BF16>(x, y);
+      if constexpr (TWO) {
+        uint32_t r = pack2<true>(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xFFFF0000u));
+        asm volatile("" : "+v"(r));
+        rest[m][i / 8][i % 8 / 2] = r;
+      }
+      asm volatile("" : "+v"(b));   // here, not where it is used
+      p[m][i / 8][i % 8 / 2] = b;
     };
     // Bits of a value that is not finite (E4M3: of a NaN, in the lowest byte).
-    auto odd_value = [](uint32_t x) {
+    auto odd_value = [](uint32_t x) INLINE {
       constexpr uint32_t E = FP8 ? 0x7Fu : BF16 ? 0x7F80u : 0x7C00u;
       return (x & E) == E;
     };
     // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN.  Returns the
     // keys of the 32 that hold one (a bit each, of the lane's own rows of the tile in LDS).
-    auto odd_values = [&](int v, int half, const uint8_t *vp) -> uint32_t {
+    auto odd_values = [&](int v, int half, const uint8_t *vp) INLINE -> uint32_t {
       bool odd = false;
 #pragma unroll
       for (int x = 0; x < CH / 2; ++x) {   // lane: key lane % 32, half of its chunks
@@ -402,30 +418,28 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       const uint64_t m = __ballot(odd);
       return (uint32_t)m | (uint32_t)(m >> 32);
     };
-    auto pv = [&](auto with_odd, const uint8_t *vp, u32x4 (*p)[2], u32x4 (*rest)[2]) {
-      static_for<2 * DN>([&](auto gc) {
-        constexpr int u = decltype(gc)::value / DN, d = decltype(gc)::value % DN;
-        u32x4 x = load_v(vp, u, d);
-        if constexpr (decltype(with_odd)::value) {   // without the values that are not finite
+    // One load's share of O^T += V^T P^T
+    auto pv = [&](auto with_odd, auto gc, u32x4 x) INLINE {
+      constexpr int u = decltype(gc)::value / DN, d = decltype(gc)::value % DN;
+      if constexpr (decltype(with_odd)::value) {   // without the values that are not finite
 #pragma unroll
-          for (int i = 0; i < (FP8 ? 2 : 4); ++i)
+        for (int i = 0; i < (FP8 ? 2 : 4); ++i)
 #pragma unroll
-            for (int y = 0; y < 32; y += FP8 ? 8 : 16)
-              if (odd_value((x[i] >> y) & 0xFFFFu)) x[i] &= ~((FP8 ? 0xFFu : 0xFFFFu) << y);
-        }
-        if constexpr (FP8)
-          x = u32x4{codes2<true, false>(x.x), codes2<true, true>(x.x), codes2<true, false>(x.y), codes2<true, true>(x.y)};
+          for (int y = 0; y < 32; y += FP8 ? 8 : 16)
+            if (odd_value((x[i] >> y) & 0xFFFFu)) x[i] &= ~((FP8 ? 0xFFu : 0xFFFFu) << y);
+      }
+      if constexpr (FP8)
+        x = u32x4{codes2<true, false>(x.x), codes2<true, true>(x.x), codes2<true, false>(x.y), codes2<true, true>(x.y)};
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          o[m][d] = mfma32<PV_BF16>(x, p[m][u], o[m][d]);
-          if constexpr (TWO) o[m][d] = mfma32<true>(x, rest[m][u], o[m][d]);
-        }
-      });
+      for (int m = 0; m < 2; ++m) {
+        o[m][d] = mfma32<PV_BF16>(x, p[m][u], o[m][d]);
+        if constexpr (TWO) o[m][d] = mfma32<true>(x, rest[m][u], o[m][d]);
+      }
     };
     // The values left out, key by key, for the rows that see them: weights x values by the vector unit
-    auto add_odd = [&](int v, int half, const uint8_t *vp, u32x4 (*p)[2], u32x4 (*rest)[2], uint32_t odd) {
+    auto add_odd = [&](int v, int half, const uint8_t *vp, uint32_t odd) INLINE {
       const int32_t k0 = key0(v) + 32 * half;
-      const uint32_t good = good_keys(v, half);
+      const uint32_t good = (uint32_t)(good_keys(v) >> (32 * half));
       while (odd) {
         const int key = __builtin_ctz(odd);
         odd &= odd - 1;
@@ -474,51 +488,120 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     };
 
     meet();
-    qk(lds, sa);
-    k_scales(0, 0, sa);
-    masked = mask(0, 0, sa);
-    {
-      float top[2];
-      first_max(sa, top);
-      settle(sa, top);
-    }
+    static_for<NKL>([&](auto g) INLINE { qk(g, load_k(lds, decltype(g)::value), sa); });
+    float top[2];
+    if constexpr (FP8)
+      for (int x = 0; x < 4; ++x) {
+        const f32x4 f = scales_at(0, 0, x, 0);
+        for (int i = 0; i < 4; ++i) {
+          sa[0][4 * x + i] *= f[i];
+          sa[1][4 * x + i] *= f[i];
+        }
+      }
+    uint64_t good = good_keys(0);
+    int32_t k0 = key0(0);
+    masked = mask(k0, (uint32_t)good, sa);
+    first_max(sa, top);
+    settle(sa, top);
+    // Operands are read two products ahead
+    u32x4 kf[2] = {load_k(lds + 32 * RB, 0), load_k(lds + 32 * RB, 1)}, vf[2];
+    // Between two fences go two products and their share of the other work: the matrix unit is never without either
+    auto fence = []() INLINE { __builtin_amdgcn_sched_barrier(0); };
     for (int j = 0; j < nv; ++j) {
       if (j > 0) meet();
-      const int vn = vs == 0 ? 2 : vs - 1;
-      request_scales(j + 3);
-#pragma unroll
-      for (int u = 0; u < NI; ++u) request_k(j + 3, (j + 3) & (KSTAGES - 1), u);
-#pragma unroll
-      for (int u = 0; u < NI; ++u) request_v(j + 2, vn, u);
-      request_ids(j + 5);
-      const uint8_t *kp = lds + (j & (KSTAGES - 1)) * KV, *kn = lds + ((j + 1) & (KSTAGES - 1)) * KV, *vp = lds + V_AT + vs * KV;
-      auto half = [&](auto hc, f32x16 *cur, f32x16 *nxt) {
+      const uint8_t *kp = lds + (j & (KSTAGES - 1)) * KV, *kn = lds + ((j + 1) & (KSTAGES - 1)) * KV, *vp = lds + V_AT + vst * KV;
+      // 32 keys: their weights and second product, beside the first product of the next 32
+      auto half = [&](auto hc, f32x16 *cur, f32x16 *nxt) INLINE {
         constexpr int hh = decltype(hc)::value;
-        u32x4 p[2][2], rest[2][2];
-        qk(hh == 0 ? kp + 32 * RB : kn, nxt);
-        weights(j, hh, cur, p, rest);
-        k_scales(j + hh, 1 - hh, nxt);
-        uint32_t odd = 0;
-        if (masked) odd = odd_values(j, hh, vp + hh * 32 * RB);
-        const bool m2 = mask(j + hh, 1 - hh, nxt);
+        constexpr int NB = 2 * DN, EARLY = 12;   // pairs of weights in the first part, of 16
+        const uint8_t *kc = hh == 0 ? kp + 32 * RB : kn, *kd = hh == 0 ? kn : kn + 32 * RB, *vc = vp + hh * 32 * RB;
+        if constexpr (FP8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) vsc[x] = scales_at(j, hh, x, 1);
+          if (masked) {   // scales that are not finite reach the rows that see their keys through add_odd
+            asm volatile("");
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) vsc[x][i] = vsc[x][i] - vsc[x][i] == 0.f ? vsc[x][i] : 0.f;
+          }
+        }
+        fence();
+        static_for<NKL>([&](auto gc) INLINE {
+          constexpr int g = decltype(gc)::value;
+          qk(gc, kf[g & 1], nxt);
+          if constexpr (g + 2 < NKL)
+            kf[g & 1] = load_k(kc, g + 2);
+          else
+            vf[g & 1] = load_v(vc, (g + 2 - NKL) / DN, (g + 2 - NKL) % DN);
+          static_for<(g + 1) * EARLY / NKL - g * EARLY / NKL>([&](auto n) INLINE { weigh(g * EARLY / NKL + decltype(n)::value, cur); });
+          if constexpr (hh == 0) {
+            if constexpr (g == 0) request_scales(j + 3);
+            if constexpr (g % (NKL / NI) == 0) request_k((j + 3) & (KSTAGES - 1), ks, g / (NKL / NI));
+          } else {
+            if constexpr (g == 0) request_ids(j + 6);
+            if constexpr (g % (NKL / NI) == 0) request_v(vst == 0 ? 2 : vst - 1, vs, g / (NKL / NI));
+          }
+          fence();
+        });
+        const uint32_t odd = masked ? odd_values(j, hh, vc) : 0u;
         if (odd) {
           asm volatile("");
-          pv(std::true_type{}, vp + hh * 32 * RB, p, rest);
-          add_odd(j, hh, vp + hh * 32 * RB, p, rest, odd);
+          static_for<16 - EARLY>([&](auto n) INLINE { weigh(EARLY + decltype(n)::value, cur); });
+          static_for<NB>([&](auto g) INLINE { pv(std::true_type{}, g, load_v(vc, decltype(g)::value / DN, decltype(g)::value % DN)); });
+          add_odd(j, hh, vc, odd);
+          kf[0] = load_k(kd, 0);
+          kf[1] = load_k(kd, 1);
+          if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float f = scales_at(j + hh, 1 - hh, i / 4, 0)[i % 4];
+              nxt[0][i] *= f;
+              nxt[1][i] *= f;
+            }
+          }
+          first_max(nxt, top);
         } else {
-          pv(std::false_type{}, vp + hh * 32 * RB, p, rest);
+          fence();
+          static_for<NB>([&](auto gc) INLINE {
+            constexpr int g = decltype(gc)::value;
+            pv(std::false_type{}, gc, vf[g & 1]);
+            if constexpr (g + 2 < NB)
+              vf[g & 1] = load_v(vc, (g + 2) / DN, (g + 2) % DN);
+            else
+              kf[g & 1] = load_k(kd, g + 2 - NB);
+            constexpr int LATE = 16 - EARLY, ON = NB / 2;   // the first 16 keys' products need no more weights
+            if constexpr (g < ON)
+              static_for<(g + 1) * LATE / ON - g * LATE / ON>([&](auto n) INLINE { weigh(EARLY + g * LATE / ON + decltype(n)::value, cur); });
+            static_for<16 / NB>([&](auto ic) INLINE {
+              constexpr int i = g * (16 / NB) + decltype(ic)::value;
+              if constexpr (FP8) {
+                const float f = scales_at(j + hh, 1 - hh, i / 4, 0)[i % 4];
+                nxt[0][i] *= f;
+                nxt[1][i] *= f;
+              }
+#pragma unroll
+              for (int m = 0; m < 2; ++m) top[m] = i == 0 ? nxt[m][0] : __builtin_fmaxf(top[m], nxt[m][i]);
+            });
+            fence();
+          });
         }
-        masked = m2;
-        float top[2];
-        first_max(nxt, top);
-        sc[0] = sc[1] = a.scale2;
-        nb[0] = ref[0] == NEG_INF ? 0.f : -ref[0];
-        nb[1] = ref[1] == NEG_INF ? 0.f : -ref[1];
+        if constexpr (hh == 1) {
+          vs = ks;
+          ks = slots_of(j + 4);
+          good = good_keys(j + 1);
+          k0 = key0(j + 1);
+        }
+        masked = mask(k0 + 32 * (1 - hh), (uint32_t)(good >> (32 * (1 - hh))), nxt);
+        if (masked) {
+          asm volatile("");
+          first_max(nxt, top);
+        }
         settle(nxt, top);
       };
       half(std::integral_constant<int, 0>{}, sa, sb);
       half(std::integral_constant<int, 1>{}, sb, sa);
-      vs = vs == 2 ? 0 : vs + 1;
+      vst = vst == 2 ? 0 : vst + 1;
     }
   }
   copies_left<0>();   // none may write LDS that is another workgroup's by then
@@ -554,7 +637,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
 
 template <bool BF16, bool FP8, int D>
 hipError_t launch_one(const PagedArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL((chunk_kernel<BF16, FP8, D>), dim3((unsigned)a.max_items), dim3(64 * WAVES), (chunk_lds<FP8, D>()), s, a);
+  const dim3 grid((unsigned)a.max_items), block(64 * WAVES);
+  constexpr int lds = chunk_lds<FP8, D>();
+  if (a.page_sh >= 4 && a.rows >> a.page_sh << a.page_sh == a.rows)
+    hipLaunchKernelGGL((chunk_kernel<BF16, FP8, D, true>), grid, block, lds, s, a);
+  else
+    hipLaunchKernelGGL((chunk_kernel<BF16, FP8, D, false>), grid, block, lds, s, a);
   return hipGetLastError();
 }
 

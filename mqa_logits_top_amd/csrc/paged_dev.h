@@ -55,6 +55,17 @@ struct Item {
   int32_t next;            // items from one split of a tile to the next
 };
 
+// The same in scalar registers.
+__device__ __forceinline__ int32_t uniform(int32_t x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+  const uint64_t x = (uint64_t)p;
+  return (const uint8_t *)((uint64_t)(uint32_t)uniform((int32_t)(x >> 32)) << 32 | (uint32_t)uniform((int32_t)x));
+}
+__device__ __forceinline__ Item uniform(const Item &w) {
+  return {{uniform(w.r.from), uniform(w.r.n), uniform(w.r.len)}, uniform(w.b),          uniform(w.row0), uniform(w.split),
+          uniform(w.splits),                                     uniform(w.first_item), uniform(w.next)};
+}
+
 __device__ __forceinline__ int32_t wave_sum_i(int32_t x) { return (int32_t)wave_sum((uint32_t)x); }
 
 // The id-th item (or, with TILES, the id-th row tile) of the launch's list; false: there is none.  Every lane of the wave
