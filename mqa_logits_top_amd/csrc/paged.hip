@@ -80,15 +80,16 @@ __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
 PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len) {
   PagedPlan p{};
   const int32_t live = B < T ? (B > 0 ? B : 1) : (T > 0 ? T : 1);   // requests that can have rows
-  p.chunk = true;
-  p.M = 256;
+  const int64_t need = (int64_t)((T + live - 1) / live) * G;        // rows of a request and cache head, about
+  p.chunk = need > 32;
+  p.M = p.chunk ? 256 : need > 16 ? 32 : 16;
   p.Gt = G < p.M ? G : p.M;
   p.blocks = (G + p.Gt - 1) / p.Gt;
   p.R = p.M / p.Gt;
   const int64_t mu = (int64_t)Hkv * p.blocks;
   const int32_t kt = p.chunk ? 64 : 32;
   p.slots = p.chunk ? (D == 64 ? 512 : 256) : 1024;
-  p.min_tiles = 8;
+  p.min_tiles = p.chunk ? 8 : 4;
   const int64_t divided = (T / p.R + live) * mu;      // row tiles at most
   p.divide = divided < 3 * p.slots && max_len > 2 * p.min_tiles * kt && B <= 4096;
   if (p.divide) {
@@ -121,7 +122,7 @@ hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, con
   a.max_items = (int32_t)plan.max_items;
   a.part = (float *)ws;
   a.part_ml = a.part + (size_t)plan.max_items * plan.M * D;
-  const hipError_t e = launch_paged_chunk(a, dtype, fmt, D, s);
+  const hipError_t e = plan.chunk ? launch_paged_chunk(a, dtype, fmt, D, s) : launch_paged_step(a, dtype, fmt, D, plan.M, s);
   if (e != hipSuccess || !plan.divide) return e;
   if (D == 64) return dtype == IDX_K_BF16 ? launch_join<true, 64>(a, plan, s) : launch_join<false, 64>(a, plan, s);
   return dtype == IDX_K_BF16 ? launch_join<true, 128>(a, plan, s) : launch_join<false, 128>(a, plan, s);
