@@ -25,7 +25,9 @@ struct NormJob {
   int32_t group;           // values that share a scale
   int32_t T, H, D;
   float eps;
+  int32_t lanes_sh;        // log2 of the lanes of a row of up to 512 values; filled by launch_norm
+  int32_t group_sh;        // ... of the lanes of a group
 };
-hipError_t launch_norm(const NormJob &j, hipStream_t s);
+hipError_t launch_norm(NormJob &j, hipStream_t s);
 
 }  // namespace idx
