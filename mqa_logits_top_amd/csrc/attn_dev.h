@@ -37,6 +37,9 @@ __device__ __forceinline__ uint32_t codes2(uint32_t w) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
 }
 
+// By its bits: x - x of a product may become an fma, and that the product's rounding error.
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u; }
+
 // A product rounded by itself, never part of an fma.
 __device__ __forceinline__ float product(float x, float y) {
 #pragma clang fp contract(off)

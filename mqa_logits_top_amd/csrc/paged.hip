@@ -17,8 +17,9 @@ __global__ __launch_bounds__(JOIN) void join_kernel(PagedArgs a, int M, int slic
   const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
   const uint32_t member = blockIdx.x % mu, rest = blockIdx.x / mu;
   const int slice = (int)(rest % (uint32_t)slices);
-  Item w;
-  if (!find_item<KT, CHUNK, true>(a, rest / (uint32_t)slices, w) || w.splits == 1) return;
+  Item found;
+  if (!find_item<KT, CHUNK, true>(a, rest / (uint32_t)slices, found) || found.splits == 1) return;
+  const Item w = uniform(found);
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   const int heads = min(a.Gt, a.G - hb * a.Gt), d = 4 * (threadIdx.x % QUADS);
   for (int row = slice * (M / slices) + threadIdx.x / QUADS; row < (slice + 1) * (M / slices); row += JOIN / QUADS) {

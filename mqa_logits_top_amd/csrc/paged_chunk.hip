@@ -70,38 +70,40 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
   const uint32_t member = blockIdx.x % mu;
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
-  Item w;
-  if (!find_item<KT, true, false>(a, blockIdx.x / mu, w)) return;
-  w = uniform(w);
+  Item found;
+  if (!find_item<KT, true, false>(a, blockIdx.x / mu, found)) return;
+  const Item w = uniform(found);
   const int head0 = kvh * a.G + hb * a.Gt, heads = min(a.Gt, a.G - hb * a.Gt);
   const KeyTiles kt = key_tiles<KT>(a, w.r, w.row0, a.R);
   const int v0 = (int)((int64_t)kt.count * w.split / w.splits), v1 = (int)((int64_t)kt.count * (w.split + 1) / w.splits);
   const int nv = v1 - v0;
 
-  // this lane's rows
+  // this lane's rows: the m-th of them is row 64 wave + 32 m + l % 32 of the tile
+  struct Row {
+    int32_t t, h;             // token and query head
+    bool real;
+  };
+  auto row_of = [&](int m) INLINE -> Row {
+    const int row = wave * 64 + m * 32 + c, tok = row / a.Gt, h = row - tok * a.Gt;
+    return {w.r.from + w.row0 + tok, head0 + h, tok < a.R && h < heads && w.row0 + tok < w.r.n};
+  };
   int32_t pos[2], lb[2];      // last key a row sees; keys above lb, or below a.first, are in its window
-  int64_t q_at[2];
-  int32_t t[2], h[2];
-  bool real[2];
   int32_t min_pos = INT32_MAX, max_lb = -1;
+  bool some = false;
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const int row = wave * 64 + m * 32 + c, tok = row / a.Gt;
-    h[m] = row - tok * a.Gt;
-    real[m] = tok < a.R && h[m] < heads && w.row0 + tok < w.r.n;
-    t[m] = w.r.from + w.row0 + tok;
-    h[m] += head0;
-    pos[m] = real[m] ? w.r.len - w.r.n + w.row0 + tok : -1;
-    lb[m] = a.window && real[m] ? (int32_t)max((int64_t)pos[m] - a.window, (int64_t)-1) : -1;
-    q_at[m] = (int64_t)t[m] * a.q_t + (int64_t)h[m] * a.q_h;
-    if (real[m]) {
+    const Row r = row_of(m);
+    pos[m] = r.real ? w.r.len - w.r.n + (r.t - w.r.from) : -1;
+    lb[m] = a.window && r.real ? (int32_t)max((int64_t)pos[m] - a.window, (int64_t)-1) : -1;
+    if (r.real) {
       min_pos = min(min_pos, pos[m]);
       max_lb = max(max_lb, lb[m]);
+      some = true;
     }
   }
-  min_pos = __builtin_amdgcn_readfirstlane((int)(wave_min((uint32_t)min_pos ^ 0x80000000u) ^ 0x80000000u));
-  max_lb = __builtin_amdgcn_readfirstlane((int)(wave_max((uint32_t)(max_lb + 1)) - 1u));
-  const bool any_row = __any(real[0] || real[1]);
+  min_pos = uniform((int32_t)(wave_min((uint32_t)min_pos ^ 0x80000000u) ^ 0x80000000u));
+  max_lb = uniform((int32_t)(wave_max((uint32_t)(max_lb + 1)) - 1u));
+  const bool any_row = __any(some);
 
   // ---- copies
   const int32_t *table = a.pages + (int64_t)w.b * a.ld_pages;
@@ -213,9 +215,66 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NSTEP) : "memory");
   };
   int vst = 0;        // stage of V(j)
+  // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN.  Before such a tile
+  // is used each wave takes them out of its rows of it in LDS; at the end the rows that see them get them.
+  bool odd_seen = false;
+  const int32_t p0 = w.r.len - w.r.n + w.row0, p1 = last_key;   // the workgroup's first and last row
+  const int32_t lb1 = a.window ? (int32_t)max((int64_t)p1 - a.window, (int64_t)-1) : -1;
+  auto good_keys = [&](int v) INLINE -> uint64_t {   // keys of a tile that have a slot
+    const uint32_t id = ids[(v & (IDS - 1)) * KT + lane];
+    if constexpr (RUNS) return __ballot(id <= max_page);
+    bool ok;
+    slot_of(id, min(key0(v) + lane, last_key), ok);
+    return __ballot(ok);
+  };
+  auto clean = [&](int v, int32_t k0, uint64_t good) INLINE {
+    if (k0 + KT - 1 <= p0 && (k0 > lb1 || k0 + KT - 1 < a.first) && good == ~0ull) return;
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NSTEP) : "memory");   // its own rows are there
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < CH / 4; ++i) {
+      u32x4 *const at = (u32x4 *)(lds + V_AT + vst * KV + 16 * wave * RB) + i * 64 + lane;
+      u32x4 z = *at;
+      bool here = false;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t bits;   // of the values that are not finite (E4M3: of NaNs)
+        if constexpr (FP8) {
+          bits = ((((z[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+        } else {
+          constexpr uint32_t E = BF16 ? 0x7F80u : 0x7C00u;
+          bits = ((z[x] & E) == E ? 0xFFFFu : 0u) | ((z[x] >> 16 & E) == E ? 0xFFFF0000u : 0u);
+        }
+        z[x] &= ~bits;
+        here |= bits != 0u;
+      }
+      if (here) *at = z;
+      odd |= here;
+    }
+    if constexpr (FP8) {
+      float *const at = (float *)(lds + SCALES_AT + ((v & (KSTAGES - 1)) * WAVES + wave) * 256) + 16 + (lane & 15);
+      if (!finite(*at)) {
+        *at = 0.f;
+        odd = true;
+      }
+    }
+    odd_seen |= __any(odd) != 0;
+    lds_done();
+  };
+  uint64_t good = 0;
+  int32_t k0 = 0;
+  if (nv > 0) {
+    good = good_keys(0);
+    k0 = key0(0);
+    clean(0, k0, good);
+  }
   if (!any_row) {
     // no row of its own: the wave's share of the copies only
     for (int j = 0; j < nv; ++j) {
+      if (j > 0) {
+        good = good_keys(j);
+        clean(j, key0(j), good);
+      }
       meet();
       request_scales(j + 3);
 #pragma unroll
@@ -231,45 +290,46 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     // Q^T as B operands: lane l holds row l % 32 and 8 dims of each 16
     u32x4 q[2][KS];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < 2; ++m) {
+      const Row r = row_of(m);
+      const uint8_t *at = a.q + (r.real ? (int64_t)r.t * a.q_t + (int64_t)r.h * a.q_h : 0);
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         const int e = FP8 ? 32 * (s >> 1) + 16 * hl + 8 * (s & 1) : 16 * s + 8 * hl;
-        u32x4 x = {0u, 0u, 0u, 0u};
-        if (real[m]) x = *(const u32x4 *)(a.q + q_at[m] + 2 * e);
-        q[m][s] = (x & a.q_keep) ^ a.q_sign;
+        q[m][s] = *(const u32x4 *)(at + 2 * e);   // rows that are not there: any row's, masked and not stored
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        q[m][s] = (q[m][s] & a.q_keep) ^ a.q_sign;
         // with 128 dims the queries' place is the accumulation registers, which the products read as well
         if constexpr (D == 128) asm volatile("" : "+a"(q[m][s]));
       }
-    const uint32_t k_row = (uint32_t)(c * RB), k_sw = (uint32_t)swizzle_k(c);
+    // LDS addresses of the lane's operands in the first tile.  A chunk's number enters by exclusive or, and so do the
+    // swizzles: the next operand's address is one exclusive or with a constant away.
+    const uint32_t k_lane = lds_addr(lds) + (uint32_t)(c * RB + ((hl ^ swizzle_k(c)) << 4));
     // V^T: lane 4 r + x of a group points to key r, dims 4 x (E4M3: lane 2 r + x, dims 8 x)
     const int g16 = lane & 15;
     const int vr = FP8 ? (g16 >> 1) : (g16 >> 2);
     const int vkey = FP8 ? (vr < 4 ? 4 * hl + vr : 4 + 4 * hl + vr) : 4 * hl + vr;   // of the 16 (FP8) or of each 8
-    const uint32_t v_row = (uint32_t)(vkey * RB + 8 * (g16 & 1));
-    const uint32_t v_ch = FP8 ? (uint32_t)((lane >> 4) & 1) : (uint32_t)(2 * ((lane >> 4) & 1) + ((g16 & 3) >> 1));
-    const uint32_t v_sw = (uint32_t)swizzle_v(vkey);
+    const int v_ch = FP8 ? (lane >> 4) & 1 : 2 * ((lane >> 4) & 1) + ((g16 & 3) >> 1);
+    const uint32_t v_lane =
+        lds_addr(lds) + (uint32_t)(V_AT + vkey * RB + 8 * (g16 & 1) + ((v_ch ^ swizzle_v(vkey)) << 4));
 
-    float sc[2] = {a.scale2, a.scale2}, nb[2] = {0.f, 0.f};
-    bool big = false, masked = false;
+    float nb[2] = {0.f, 0.f};   // -ref, or 0 while there is none
+    bool big = false;
 
-    auto load_k = [&](const uint8_t *kp, int g) INLINE {
-      return *(const u32x4 *)(kp + k_row + (((uint32_t)(2 * g + hl) ^ k_sw) << 4));
-    };
+    typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+    // K of 16 dims (E4M3: 32) from 16 g (32 g) on; at: k_lane in the tile and half
+    auto load_k = [&](uint32_t at, int g) INLINE { return *(lds_u32x4 *)(uintptr_t)(at ^ (uint32_t)(32 * g)); };
     // scores of 32 keys: S^T = K Q^T
     f32x16 sa[2], sb[2];
     auto scales_at = [&](int v, int half, int x, int value) INLINE {   // of keys 32 half + 8 x + 4 (l / 32) .. + 3
       const float *p = (const float *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256) + 16 * value;
       const int key = 32 * half + 8 * x + 4 * hl;
       return *(const f32x4 *)(p + (key >> 4) * 64 + (key & 15));
-    };
-    // which keys of a tile have a slot
-    auto good_keys = [&](int v) INLINE -> uint64_t {
-      const uint32_t id = ids[(v & (IDS - 1)) * KT + lane];
-      if constexpr (RUNS) return __ballot(id <= max_page);
-      bool ok;
-      slot_of(id, min(key0(v) + lane, last_key), ok);
-      return __ballot(ok);
     };
     // 32 keys from k0 on: every row sees them all if k0 is one of these, and the slots are good
     const uint32_t whole0 = min_pos - 31 > max_lb ? (uint32_t)max_lb + 1u : ~0u;
@@ -284,7 +344,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         const int32_t key = k0 + off + 4 * hl;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-          const bool sees = key <= pos[m] && (key > lb[m] || key < a.first) && ((mine >> off) & 1u);
+          const bool sees = (key <= pos[m]) & ((key > lb[m]) | (key < a.first)) & ((mine >> off) & 1u);
           s[m][i] = sees ? s[m][i] : NEG_INF;
         }
       }
@@ -308,21 +368,20 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           ref[m] = to;
           const bool rounds = __builtin_fabsf(to) >= BIG && to != NEG_INF;   // then every tile is looked at
           high[m] = rounds ? NEG_INF : (to + (8.f + LIFT)) / a.scale2;
-          sc[m] = a.scale2;
           nb[m] = to == NEG_INF ? 0.f : -to;
           far |= rounds;
         }
         big = __any(far);
       }
       if (big) {
-        // The reference's own rounding passes the exponential's range: products are rounded like it, then it is taken off
+        // The reference's own rounding passes the exponential's range: products are rounded like it, then it is taken off.
+        // (What is left is small where it matters, and comes back through the scale within 2^-22 of itself.)
         asm volatile("");
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const bool far = __builtin_fabsf(ref[m]) >= BIG && ref[m] != NEG_INF;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[m][i] = far ? product(s[m][i], a.scale2) - ref[m] : s[m][i];
-          sc[m] = far ? 1.f : a.scale2;
+          for (int i = 0; i < 16; ++i) s[m][i] = far ? (product(s[m][i], a.scale2) - ref[m]) / a.scale2 : s[m][i];
           nb[m] = far || ref[m] == NEG_INF ? 0.f : -ref[m];
         }
       }
@@ -351,19 +410,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         for (int m = 0; m < 2; ++m) s[m] = mfma32<BF16>(x, q[m][g], s[m]);
       }
     };
-    // V^T of dims 32 d .. and the 16 keys from 16 u on
-    auto load_v = [&](const uint8_t *vp, int u, int d) INLINE -> u32x4 {
+    // V^T of dims 32 d .. and the 16 keys from 16 u on; at: v_lane in the tile and half
+    auto load_v = [&](uint32_t at, int u, int d) INLINE -> u32x4 {
       if constexpr (FP8) {
         const i32x2 x = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2 *)(vp + 16 * u * RB + v_row + (((uint32_t)(2 * d) + v_ch) ^ v_sw) * 16));
+            (__attribute__((address_space(3))) i32x2 *)(uintptr_t)((at ^ (uint32_t)(32 * d)) + 16 * u * RB));
         return u32x4{(uint32_t)x[0], (uint32_t)x[1], 0u, 0u};
       } else {
         u32x4 r;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const i32x2 x = __builtin_bit_cast(
-              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(
-                         vp + (16 * u + 8 * e) * RB + v_row + (((uint32_t)(4 * d) + v_ch) ^ v_sw) * 16)));
+              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4 *)(uintptr_t)(
+                         (at ^ (uint32_t)(64 * d)) + (16 * u + 8 * e) * RB)));
           r[2 * e] = (uint32_t)x[0];
           r[2 * e + 1] = (uint32_t)x[1];
         }
@@ -375,8 +434,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     // Weights of two keys, the n-th pair of the 16: keys in the order of the second product's steps
     auto weigh = [&](int n, const f32x16 *s) INLINE {
       const int m = n & 1, i = n >> 1 << 1;
-      float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i], sc[m], nb[m]));
-      float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i + 1], sc[m], nb[m]));
+      float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i], a.scale2, nb[m]));
+      float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i + 1], a.scale2, nb[m]));
       sum[m] += x;
       sum[m] += y;
       if constexpr (FP8) {
@@ -392,42 +451,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       asm volatile("" : "+v"(b));   // here, not where it is used
       p[m][i / 8][i % 8 / 2] = b;
     };
-    // Bits of a value that is not finite (E4M3: of a NaN, in the lowest byte).
-    auto odd_value = [](uint32_t x) INLINE {
-      constexpr uint32_t E = FP8 ? 0x7Fu : BF16 ? 0x7F80u : 0x7C00u;
-      return (x & E) == E;
-    };
-    // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN.  Returns the
-    // keys of the 32 that hold one (a bit each, of the lane's own rows of the tile in LDS).
-    auto odd_values = [&](int v, int half, const uint8_t *vp) INLINE -> uint32_t {
-      bool odd = false;
-#pragma unroll
-      for (int x = 0; x < CH / 2; ++x) {   // lane: key lane % 32, half of its chunks
-        const u32x4 z = *(const u32x4 *)(vp + c * RB + (hl * (CH / 2) + x) * 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int y = 0; y < 32; y += FP8 ? 8 : 16) odd |= odd_value(z[i] >> y);
-      }
-      if constexpr (FP8) {
-        const int key = 32 * half + c;
-        const uint32_t e = ((const uint32_t *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256))[(key >> 4) * 64 + 16 +
-                                                                                                     (key & 15)];
-        odd |= (e & 0x7F800000u) == 0x7F800000u;
-      }
-      const uint64_t m = __ballot(odd);
-      return (uint32_t)m | (uint32_t)(m >> 32);
-    };
     // One load's share of O^T += V^T P^T
-    auto pv = [&](auto with_odd, auto gc, u32x4 x) INLINE {
+    auto pv = [&](auto gc, u32x4 x) INLINE {
       constexpr int u = decltype(gc)::value / DN, d = decltype(gc)::value % DN;
-      if constexpr (decltype(with_odd)::value) {   // without the values that are not finite
-#pragma unroll
-        for (int i = 0; i < (FP8 ? 2 : 4); ++i)
-#pragma unroll
-          for (int y = 0; y < 32; y += FP8 ? 8 : 16)
-            if (odd_value((x[i] >> y) & 0xFFFFu)) x[i] &= ~((FP8 ? 0xFFu : 0xFFFFu) << y);
-      }
       if constexpr (FP8)
         x = u32x4{codes2<true, false>(x.x), codes2<true, true>(x.x), codes2<true, false>(x.y), codes2<true, true>(x.y)};
 #pragma unroll
@@ -436,59 +462,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         if constexpr (TWO) o[m][d] = mfma32<true>(x, rest[m][u], o[m][d]);
       }
     };
-    // The values left out, key by key, for the rows that see them: weights x values by the vector unit
-    auto add_odd = [&](int v, int half, const uint8_t *vp, uint32_t odd) INLINE {
-      const int32_t k0 = key0(v) + 32 * half;
-      const uint32_t good = (uint32_t)(good_keys(v) >> (32 * half));
-      while (odd) {
-        const int key = __builtin_ctz(odd);
-        odd &= odd - 1;
-        // the weight is the i-th of lane half own
-        const int i = 4 * (key >> 3) + (key & 3), own = (key >> 2) & 1;
-        const float vs1 = FP8 ? ((const float *)(lds + SCALES_AT + (v & (KSTAGES - 1)) * WAVES * 256))[((32 * half + key) >> 4) * 64 + 16 + (key & 15)] : 1.f;
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          uint32_t word = 0, less = 0;
-#pragma unroll
-          for (int z = 0; z < 8; ++z)
-            if (z == (i >> 1)) {
-              word = p[m][z / 4][z % 4];
-              if constexpr (TWO) less = rest[m][z / 4][z % 4];
-            }
-          const uint32_t bits = (i & 1) ? word >> 16 : word & 0xFFFFu;
-          float wgt = PV_BF16 ? __uint_as_float(bits << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
-          if constexpr (TWO) wgt += __uint_as_float((i & 1) ? less & 0xFFFF0000u : less << 16);
-          const uint32_t wu = __float_as_uint(wgt);
-          const auto sw = __builtin_amdgcn_permlane32_swap(wu, wu, false, false);
-          wgt = __uint_as_float(own ? sw[1] : sw[0]);
-          const int32_t s = k0 + key;
-          const bool sees = s <= pos[m] && (s > lb[m] || s < a.first) && ((good >> key) & 1u);
-          if (FP8 && !(vs1 - vs1 == 0.f)) wgt = vs1;   // a scale that is not finite makes the whole row so
-#pragma unroll
-          for (int d = 0; d < DN; ++d)
-#pragma unroll
-            for (int z = 0; z < 16; ++z) {
-              const int dim = 32 * d + 8 * (z / 4) + 4 * hl + z % 4;
-              const int chunk = (dim * (FP8 ? 1 : 2) / 16) ^ swizzle_v(key);
-              const uint8_t *at = vp + key * RB + chunk * 16 + (dim * (FP8 ? 1 : 2)) % 16;
-              float val;
-              bool left;
-              if constexpr (FP8) {
-                val = __builtin_amdgcn_cvt_f32_fp8((int)*at, 0);
-                left = odd_value(*at) || !(vs1 - vs1 == 0.f);
-              } else {
-                const uint32_t x = *(const uint16_t *)at;
-                val = BF16 ? __uint_as_float(x << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)x);
-                left = odd_value(x);
-              }
-              if (sees && left) o[m][d][z] = __builtin_fmaf(wgt, val, o[m][d][z]);
-            }
-        }
-      }
-    };
-
     meet();
-    static_for<NKL>([&](auto g) INLINE { qk(g, load_k(lds, decltype(g)::value), sa); });
+    static_for<NKL>([&](auto g) INLINE { qk(g, load_k(k_lane, decltype(g)::value), sa); });
     float top[2];
     if constexpr (FP8)
       for (int x = 0; x < 4; ++x) {
@@ -498,43 +473,31 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           sa[1][4 * x + i] *= f[i];
         }
       }
-    uint64_t good = good_keys(0);
-    int32_t k0 = key0(0);
-    masked = mask(k0, (uint32_t)good, sa);
+    mask(k0, (uint32_t)good, sa);
     first_max(sa, top);
     settle(sa, top);
     // Operands are read two products ahead
-    u32x4 kf[2] = {load_k(lds + 32 * RB, 0), load_k(lds + 32 * RB, 1)}, vf[2];
+    u32x4 kf[2] = {load_k(k_lane + 32 * RB, 0), load_k(k_lane + 32 * RB, 1)}, vf[2];
     // Between two fences go two products and their share of the other work: the matrix unit is never without either
     auto fence = []() INLINE { __builtin_amdgcn_sched_barrier(0); };
     for (int j = 0; j < nv; ++j) {
-      if (j > 0) meet();
-      const uint8_t *kp = lds + (j & (KSTAGES - 1)) * KV, *kn = lds + ((j + 1) & (KSTAGES - 1)) * KV, *vp = lds + V_AT + vst * KV;
+      if (j > 0) {
+        clean(j, k0, good);
+        meet();
+      }
+      const uint32_t kp = k_lane + (uint32_t)((j & (KSTAGES - 1)) * KV), kn = k_lane + (uint32_t)(((j + 1) & (KSTAGES - 1)) * KV);
+      const uint32_t vp = v_lane + (uint32_t)(vst * KV);
       // 32 keys: their weights and second product, beside the first product of the next 32
       auto half = [&](auto hc, f32x16 *cur, f32x16 *nxt) INLINE {
         constexpr int hh = decltype(hc)::value;
         constexpr int NB = 2 * DN, EARLY = 12;   // pairs of weights in the first part, of 16
-        const uint8_t *kc = hh == 0 ? kp + 32 * RB : kn, *kd = hh == 0 ? kn : kn + 32 * RB, *vc = vp + hh * 32 * RB;
+        const uint32_t kc = hh == 0 ? kp + 32 * RB : kn, kd = hh == 0 ? kn : kn + 32 * RB, vc = vp + hh * 32 * RB;
         if constexpr (FP8) {
 #pragma unroll
           for (int x = 0; x < 4; ++x) vsc[x] = scales_at(j, hh, x, 1);
-          if (masked) {   // scales that are not finite reach the rows that see their keys through add_odd
-            asm volatile("");
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) vsc[x][i] = vsc[x][i] - vsc[x][i] == 0.f ? vsc[x][i] : 0.f;
-          }
         }
-        fence();
-        static_for<NKL>([&](auto gc) INLINE {
+        auto copies = [&](auto gc) INLINE {   // one load's share of the step's
           constexpr int g = decltype(gc)::value;
-          qk(gc, kf[g & 1], nxt);
-          if constexpr (g + 2 < NKL)
-            kf[g & 1] = load_k(kc, g + 2);
-          else
-            vf[g & 1] = load_v(vc, (g + 2 - NKL) / DN, (g + 2 - NKL) % DN);
-          static_for<(g + 1) * EARLY / NKL - g * EARLY / NKL>([&](auto n) INLINE { weigh(g * EARLY / NKL + decltype(n)::value, cur); });
           if constexpr (hh == 0) {
             if constexpr (g == 0) request_scales(j + 3);
             if constexpr (g % (NKL / NI) == 0) request_k((j + 3) & (KSTAGES - 1), ks, g / (NKL / NI));
@@ -542,30 +505,30 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
             if constexpr (g == 0) request_ids(j + 6);
             if constexpr (g % (NKL / NI) == 0) request_v(vst == 0 ? 2 : vst - 1, vs, g / (NKL / NI));
           }
-          fence();
-        });
-        const uint32_t odd = masked ? odd_values(j, hh, vc) : 0u;
-        if (odd) {
-          asm volatile("");
-          static_for<16 - EARLY>([&](auto n) INLINE { weigh(EARLY + decltype(n)::value, cur); });
-          static_for<NB>([&](auto g) INLINE { pv(std::true_type{}, g, load_v(vc, decltype(g)::value / DN, decltype(g)::value % DN)); });
-          add_odd(j, hh, vc, odd);
-          kf[0] = load_k(kd, 0);
-          kf[1] = load_k(kd, 1);
+        };
+        auto scale_next = [&](int i) INLINE {
           if constexpr (FP8) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float f = scales_at(j + hh, 1 - hh, i / 4, 0)[i % 4];
-              nxt[0][i] *= f;
-              nxt[1][i] *= f;
-            }
+            const float f = scales_at(j + hh, 1 - hh, i / 4, 0)[i % 4];
+            nxt[0][i] *= f;
+            nxt[1][i] *= f;
           }
-          first_max(nxt, top);
-        } else {
+        };
+        {
           fence();
+          static_for<NKL>([&](auto gc) INLINE {
+            constexpr int g = decltype(gc)::value;
+            qk(gc, kf[g & 1], nxt);
+            if constexpr (g + 2 < NKL)
+              kf[g & 1] = load_k(kc, g + 2);
+            else
+              vf[g & 1] = load_v(vc, (g + 2 - NKL) / DN, (g + 2 - NKL) % DN);
+            static_for<(g + 1) * EARLY / NKL - g * EARLY / NKL>([&](auto n) INLINE { weigh(g * EARLY / NKL + decltype(n)::value, cur); });
+            copies(gc);
+            fence();
+          });
           static_for<NB>([&](auto gc) INLINE {
             constexpr int g = decltype(gc)::value;
-            pv(std::false_type{}, gc, vf[g & 1]);
+            pv(gc, vf[g & 1]);
             if constexpr (g + 2 < NB)
               vf[g & 1] = load_v(vc, (g + 2) / DN, (g + 2) % DN);
             else
@@ -575,11 +538,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
               static_for<(g + 1) * LATE / ON - g * LATE / ON>([&](auto n) INLINE { weigh(EARLY + g * LATE / ON + decltype(n)::value, cur); });
             static_for<16 / NB>([&](auto ic) INLINE {
               constexpr int i = g * (16 / NB) + decltype(ic)::value;
-              if constexpr (FP8) {
-                const float f = scales_at(j + hh, 1 - hh, i / 4, 0)[i % 4];
-                nxt[0][i] *= f;
-                nxt[1][i] *= f;
-              }
+              scale_next(i);
 #pragma unroll
               for (int m = 0; m < 2; ++m) top[m] = i == 0 ? nxt[m][0] : __builtin_fmaxf(top[m], nxt[m][i]);
             });
@@ -592,7 +551,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           good = good_keys(j + 1);
           k0 = key0(j + 1);
         }
-        masked = mask(k0 + 32 * (1 - hh), (uint32_t)(good >> (32 * (1 - hh))), nxt);
+        const bool masked = mask(k0 + 32 * (1 - hh), (uint32_t)(good >> (32 * (1 - hh))), nxt);
         if (masked) {
           asm volatile("");
           first_max(nxt, top);
@@ -610,7 +569,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     const float l = pair_sum(sum[m]);
-    if (!real[m]) continue;
+    const Row r = row_of(m);
+    if (!r.real) continue;
     if (w.splits > 1) {
       const int64_t item = (int64_t)(w.first_item + w.split * w.next) * mu + member;
       const int64_t at = item * M + wave * 64 + m * 32 + c;
@@ -623,15 +583,72 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
               f32x4{o[m][d][z], o[m][d][z + 1], o[m][d][z + 2], o[m][d][z + 3]};
     } else {
       const float f = finish(l);
-      uint8_t *dst = a.out + (int64_t)t[m] * a.out_t + (int64_t)h[m] * a.out_h;
+      uint8_t *dst = a.out + (int64_t)r.t * a.out_t + (int64_t)r.h * a.out_h;
 #pragma unroll
       for (int d = 0; d < DN; ++d)
 #pragma unroll
         for (int z = 0; z < 16; z += 4)
           *(uint2 *)(dst + 2 * (32 * d + 2 * z + 4 * hl)) =
               make_uint2(pack2<BF16>(o[m][d][z] * f, o[m][d][z + 1] * f), pack2<BF16>(o[m][d][z + 2] * f, o[m][d][z + 3] * f));
-      if (hl == 0 && a.lse) a.lse[(int64_t)t[m] * a.Hq + h[m]] = lse_of(ref[m], l);
+      if (hl == 0 && a.lse) a.lse[(int64_t)r.t * a.Hq + r.h] = lse_of(ref[m], l);
     }
+  }
+  if (nv > 0) {   // whether any wave left some out
+    uint32_t *const word = (uint32_t *)lds;
+    __syncthreads();
+    if (threadIdx.x == 0) *word = 0u;
+    __syncthreads();
+    if (odd_seen && lane == 0) *word = 1u;
+    __syncthreads();
+    odd_seen = *word != 0u;
+  }
+  if (odd_seen) {
+    asm volatile("");   // stays a branch
+    __threadfence();    // the outputs are other lanes'
+    constexpr int E = D / 64;
+    for (int j = 0; j < nv; ++j)
+      for (int i = 0; i < KT; ++i) {
+        const int32_t key = key0(j) + i;
+        if (key > last_key) break;
+        bool ok;
+        const uint32_t slot = slot_of((uint32_t)table[key >> a.page_sh], key, ok);
+        if (!ok) continue;
+        float scale = 1.f, val[E];
+        bool odd[E], some_odd = false;
+        if constexpr (FP8) scale = a.v_scale[(int64_t)slot * a.scale_row + kvh];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const uint8_t *at = vbase + (uint64_t)slot * a.row_bytes + (lane * E + e) * (FP8 ? 1 : 2);
+          if constexpr (FP8)
+            val[e] = __builtin_amdgcn_cvt_f32_fp8((int)*at, 0) * scale;
+          else
+            val[e] = BF16 ? __uint_as_float((uint32_t) * (const uint16_t *)at << 16) : (float)*(const _Float16 *)at;
+          odd[e] = !finite(val[e]);
+          some_odd |= odd[e];
+        }
+        if (!__any(some_odd)) continue;
+        for (int row = wave * 64; row < wave * 64 + 64; ++row) {
+          const int tok = row / a.Gt, h = row - tok * a.Gt;
+          if (tok >= a.R || h >= heads || w.row0 + tok >= w.r.n) continue;
+          const int32_t p1 = w.r.len - w.r.n + w.row0 + tok;
+          if (key > p1 || (a.window && (int64_t)key <= (int64_t)p1 - a.window && key >= a.first)) continue;
+          const int64_t tq = w.r.from + w.row0 + tok;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if (!odd[e]) continue;
+            if (w.splits > 1) {
+              float *to = a.part + (((int64_t)(w.first_item + w.split * w.next) * mu + member) * M + row) * D + lane * E + e;
+              *to += val[e];
+            } else {
+              uint16_t *to = (uint16_t *)(a.out + tq * a.out_t + (int64_t)(head0 + h) * a.out_h) + lane * E + e;
+              if constexpr (BF16)
+                *to = __builtin_bit_cast(uint16_t, (__bf16)(__uint_as_float((uint32_t)*to << 16) + val[e]));
+              else
+                *to = __builtin_bit_cast(uint16_t, (_Float16)((float)__builtin_bit_cast(_Float16, *to) + val[e]));
+            }
+          }
+        }
+      }
   }
 }
 

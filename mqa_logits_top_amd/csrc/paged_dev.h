@@ -71,7 +71,7 @@ __device__ __forceinline__ int32_t wave_sum_i(int32_t x) { return (int32_t)wave_
 // The id-th item (or, with TILES, the id-th row tile) of the launch's list; false: there is none.  Every lane of the wave
 // calls it with the same id and gets the same answer.
 template <int KT, bool CHUNK, bool TILES>
-__device__ bool find_item(const PagedArgs &a, uint32_t id, Item &w) {
+__device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item &w) {
   const int lane = threadIdx.x & 63;
   const int32_t R = a.R;
   w.split = 0;

@@ -75,9 +75,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
     id = local / mu * 8 + (blockIdx.x & 7u);
     member = local % mu;
   }
-  Item w;
-  if (!find_item<KT, false, false>(a, id, w)) return;
-  w = uniform(w);
+  Item found;
+  if (!find_item<KT, false, false>(a, id, found)) return;
+  const Item w = uniform(found);
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   const int head0 = kvh * a.G + hb * a.Gt, heads = min(a.Gt, a.G - hb * a.Gt);
   const KeyTiles kt = key_tiles<KT>(a, w.r, w.row0, a.R);
@@ -295,10 +295,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
             const int32_t key = k0 + 16 * h + 4 * g + i;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const bool sees = key <= pos[m] && (key > lb[m] || key < a.first) && ((mine >> (16 * h + i)) & 1u);
+              const bool sees = (key <= pos[m]) & ((key > lb[m]) | (key < a.first)) & ((mine >> (16 * h + i)) & 1u);
               sc[m][h][i] = sees ? sc[m][h][i] : NEG_INF;
             }
-            if constexpr (FP8) vsc[h][i] = vsc[h][i] - vsc[h][i] == 0.f ? vsc[h][i] : 0.f;   // back through add_odd
+            if constexpr (FP8) vsc[h][i] = finite(vsc[h][i]) ? vsc[h][i] : 0.f;   // back through add_odd
           }
       }
       u32x4 p[MT], rest[MT];
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
 #pragma unroll
             for (int y = 0; y < 32; y += FP8 ? 8 : 16) odd |= odd_value(vt[d][i] >> y);
         const float *vs1 = (const float *)(kbuf + SCALES_AT + (j & 1) * 256) + 32;
-        if constexpr (FP8) odd |= !(vs1[lane & 31] - vs1[lane & 31] == 0.f);
+        if constexpr (FP8) odd |= !finite(vs1[lane & 31]);
         if (__any(odd)) {
           asm volatile("");
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
           for (int key = 0; key < KT; ++key) {
             float scale = 1.f;
             if constexpr (FP8) scale = vs1[key];
-            const bool bad_scale = !(scale - scale == 0.f);
+            const bool bad_scale = !finite(scale);
             const int from = ((key >> 2) & 3) * 16 + c, i = 4 * (key >> 4) + (key & 3);   // lane and weight of the row
             const int32_t s = k0 + key;
 #pragma unroll
