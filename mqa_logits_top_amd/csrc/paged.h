@@ -35,6 +35,7 @@ struct PagedArgs {
   int32_t max_items;         // workgroups of the launch
   float *part;               // divided items: [max_items][M][D] unnormalised out, then
   float *part_ml;            // [max_items][M][2] reference, sum
+  uint32_t *chunk;           // the division, for the join (0: nothing is divided)
 };
 
 struct PagedPlan {

@@ -10,15 +10,17 @@ namespace {
 
 constexpr int JOIN = 256;     // threads of a join
 
-// Joins the parts of a row tile's rows, JOIN / (D / 4) rows at a time, D / 4 threads to one.
-template <bool BF16, int D, int KT, bool CHUNK>
-__global__ __launch_bounds__(JOIN) void join_kernel(PagedArgs a, int M, int slices) {
+// Joins the parts of a row tile's rows, JOIN / (D / 4) rows at a time, D / 4 threads to one: tiles of many rows, whose keys
+// are in few parts.
+template <bool BF16, int D>
+__global__ __launch_bounds__(JOIN) void join_tile_kernel(PagedArgs a, int M, int slices) {
   constexpr int QUADS = D / 4;
   const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
   const uint32_t member = blockIdx.x % mu, rest = blockIdx.x / mu;
   const int slice = (int)(rest % (uint32_t)slices);
+  if (!*a.chunk) return;
   Item found;
-  if (!find_item<KT, CHUNK, true>(a, rest / (uint32_t)slices, found) || found.splits == 1) return;
+  if (!find_item<64, true, TILE>(a, rest / (uint32_t)slices, found) || found.splits == 1) return;
   const Item w = uniform(found);
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   const int heads = min(a.Gt, a.G - hb * a.Gt), d = 4 * (threadIdx.x % QUADS);
@@ -46,14 +48,58 @@ __global__ __launch_bounds__(JOIN) void join_kernel(PagedArgs a, int M, int slic
   }
 }
 
+// Joins the parts of one row and head, JOIN / (D / 4) of them at a time: few rows, whose keys may be in many parts.
+template <bool BF16, int D>
+__global__ __launch_bounds__(JOIN) void join_row_kernel(PagedArgs a, int M) {
+  constexpr int QUADS = D / 4, GROUPS = JOIN / QUADS;
+  __shared__ __attribute__((aligned(16))) float acc[GROUPS][D];
+  __shared__ float sums[GROUPS];
+  const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
+  const int t = (int)(blockIdx.x / (uint32_t)a.Hq), hq = (int)(blockIdx.x % (uint32_t)a.Hq);
+  if (!*a.chunk) return;
+  Item found;
+  if (!find_item<32, false, ROW>(a, (uint32_t)t, found) || found.splits == 1) return;
+  const Item w = uniform(found);
+  const int kvh = hq / a.G, hb = (hq - kvh * a.G) / a.Gt, h = hq - kvh * a.G - hb * a.Gt;
+  const int row = (t - w.r.from - w.row0) * a.Gt + h;
+  const int64_t at0 = ((int64_t)w.first_item * mu + hb * a.Hkv + kvh) * M + row, step = (int64_t)w.next * mu * M;
+  const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS, lane = threadIdx.x & 63;
+  float top = NEG_INF;   // every wave for itself
+  for (int s = lane; s < w.splits; s += 64) top = __builtin_fmaxf(top, a.part_ml[2 * (at0 + s * step)]);
+  top = wave_reduce_f32(top, [](float x, float y) { return __builtin_fmaxf(x, y); });
+  const float ref = top == NEG_INF ? 0.f : top;
+  float total = 0.f;
+  f32x4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = gr; s < w.splits; s += GROUPS) {
+    const int64_t at = at0 + s * step;
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
+    total += f * a.part_ml[2 * at + 1];
+    r += f * *(const f32x4 *)(a.part + at * D + d);
+  }
+  *(f32x4 *)&acc[gr][d] = r;
+  if (d == 0) sums[gr] = total;
+  __syncthreads();
+  if (gr) return;
+#pragma unroll
+  for (int x = 1; x < GROUPS; ++x) {
+    r += *(const f32x4 *)&acc[x][d];
+    total += sums[x];
+  }
+  r *= finish(total);
+  *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)hq * a.out_h + 2 * d) =
+      make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
+  if (d == 0 && a.lse) a.lse[(int64_t)t * a.Hq + hq] = lse_of(top, total);
+}
+
 template <bool BF16, int D>
 hipError_t launch_join(const PagedArgs &a, const PagedPlan &plan, hipStream_t s) {
-  const int slices = plan.M >= 32 ? plan.M / 32 : 1;
-  const dim3 grid((unsigned)(plan.tiles * slices));
-  if (plan.chunk)
-    hipLaunchKernelGGL((join_kernel<BF16, D, 64, true>), grid, dim3(JOIN), 0, s, a, plan.M, slices);
-  else
-    hipLaunchKernelGGL((join_kernel<BF16, D, 32, false>), grid, dim3(JOIN), 0, s, a, plan.M, slices);
+  if (plan.chunk) {
+    const int slices = plan.M * (D / 4) / JOIN;
+    hipLaunchKernelGGL((join_tile_kernel<BF16, D>), dim3((unsigned)(plan.tiles * slices)), dim3(JOIN), 0, s, a, plan.M, slices);
+  } else {
+    hipLaunchKernelGGL((join_row_kernel<BF16, D>), dim3((unsigned)((int64_t)a.T * a.Hq)), dim3(JOIN), 0, s, a, plan.M);
+  }
   return hipGetLastError();
 }
 
@@ -89,14 +135,14 @@ PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bo
   p.R = p.M / p.Gt;
   const int64_t mu = (int64_t)Hkv * p.blocks;
   const int32_t kt = p.chunk ? 64 : 32;
-  p.slots = p.chunk ? (D == 64 ? 512 : 256) : 1024;
+  p.slots = p.chunk ? (D == 64 ? 512 : 256) : 512;
   p.min_tiles = p.chunk ? 8 : 4;
   const int64_t divided = (T / p.R + live) * mu;      // row tiles at most
-  p.divide = divided < 3 * p.slots && max_len > 2 * p.min_tiles * kt && B <= 4096;
+  p.divide = divided < (p.chunk ? 3 : 6) * p.slots && max_len > 2 * p.min_tiles * kt && B <= 4096;
   if (p.divide) {
     p.tiles = divided;
-    p.max_items = divided + p.slots + p.slots / 8 + mu;
-    p.bytes = ((size_t)p.max_items * p.M * (D + 2) * 4 + 255) / 256 * 256;
+    p.max_items = divided + 2 * p.slots + p.slots / 8 + mu;
+    p.bytes = ((size_t)p.max_items * p.M * (D + 2) * 4 + 4 + 255) / 256 * 256;
   } else {
     p.tiles = (T / p.R + (int64_t)B) * mu;            // the numbers that tiles are looked up by
     p.max_items = p.tiles;
@@ -123,6 +169,7 @@ hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, con
   a.max_items = (int32_t)plan.max_items;
   a.part = (float *)ws;
   a.part_ml = a.part + (size_t)plan.max_items * plan.M * D;
+  a.chunk = (uint32_t *)(a.part_ml + (size_t)plan.max_items * plan.M * 2);
   const hipError_t e = plan.chunk ? launch_paged_chunk(a, dtype, fmt, D, s) : launch_paged_step(a, dtype, fmt, D, plan.M, s);
   if (e != hipSuccess || !plan.divide) return e;
   if (D == 64) return dtype == IDX_K_BF16 ? launch_join<true, 64>(a, plan, s) : launch_join<false, 64>(a, plan, s);

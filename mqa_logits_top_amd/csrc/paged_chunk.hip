@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   const uint32_t member = blockIdx.x % mu;
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   Item found;
-  if (!find_item<KT, true, false>(a, blockIdx.x / mu, found)) return;
+  if (!find_item<KT, true, ITEM>(a, blockIdx.x / mu, found)) return;
   const Item w = uniform(found);
   const int head0 = kvh * a.G + hb * a.Gt, heads = min(a.Gt, a.G - hb * a.Gt);
   const KeyTiles kt = key_tiles<KT>(a, w.r, w.row0, a.R);
@@ -473,13 +473,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           sa[1][4 * x + i] *= f[i];
         }
       }
-    mask(k0, (uint32_t)good, sa);
     first_max(sa, top);
-    settle(sa, top);
     // Operands are read two products ahead
     u32x4 kf[2] = {load_k(k_lane + 32 * RB, 0), load_k(k_lane + 32 * RB, 1)}, vf[2];
-    // Between two fences go two products and their share of the other work: the matrix unit is never without either
-    auto fence = []() INLINE { __builtin_amdgcn_sched_barrier(0); };
     for (int j = 0; j < nv; ++j) {
       if (j > 0) {
         clean(j, k0, good);
@@ -490,7 +486,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       // 32 keys: their weights and second product, beside the first product of the next 32
       auto half = [&](auto hc, f32x16 *cur, f32x16 *nxt) INLINE {
         constexpr int hh = decltype(hc)::value;
-        constexpr int NB = 2 * DN, EARLY = 12;   // pairs of weights in the first part, of 16
+        constexpr int NB = 2 * DN;
         const uint32_t kc = hh == 0 ? kp + 32 * RB : kn, kd = hh == 0 ? kn : kn + 32 * RB, vc = vp + hh * 32 * RB;
         if constexpr (FP8) {
 #pragma unroll
@@ -513,50 +509,51 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
             nxt[1][i] *= f;
           }
         };
-        {
-          fence();
-          static_for<NKL>([&](auto gc) INLINE {
-            constexpr int g = decltype(gc)::value;
-            qk(gc, kf[g & 1], nxt);
-            if constexpr (g + 2 < NKL)
-              kf[g & 1] = load_k(kc, g + 2);
-            else
-              vf[g & 1] = load_v(vc, (g + 2 - NKL) / DN, (g + 2 - NKL) % DN);
-            static_for<(g + 1) * EARLY / NKL - g * EARLY / NKL>([&](auto n) INLINE { weigh(g * EARLY / NKL + decltype(n)::value, cur); });
-            copies(gc);
-            fence();
-          });
-          static_for<NB>([&](auto gc) INLINE {
-            constexpr int g = decltype(gc)::value;
-            pv(gc, vf[g & 1]);
-            if constexpr (g + 2 < NB)
-              vf[g & 1] = load_v(vc, (g + 2) / DN, (g + 2) % DN);
-            else
-              kf[g & 1] = load_k(kd, g + 2 - NB);
-            constexpr int LATE = 16 - EARLY, ON = NB / 2;   // the first 16 keys' products need no more weights
-            if constexpr (g < ON)
-              static_for<(g + 1) * LATE / ON - g * LATE / ON>([&](auto n) INLINE { weigh(EARLY + g * LATE / ON + decltype(n)::value, cur); });
-            static_for<16 / NB>([&](auto ic) INLINE {
-              constexpr int i = g * (16 / NB) + decltype(ic)::value;
-              scale_next(i);
+        auto first_product = [&](auto gc) INLINE {   // one load's share, and the next but one's operands
+          constexpr int g = decltype(gc)::value;
+          qk(gc, kf[g & 1], nxt);
+          if constexpr (g + 2 < NKL)
+            kf[g & 1] = load_k(kc, g + 2);
+          else
+            vf[g & 1] = load_v(vc, (g + 2 - NKL) / DN, (g + 2 - NKL) % DN);
+          copies(gc);
+        };
+        // A few products ahead of what the weights wait for: the mask, the maximum against the reference
+        constexpr int AHEAD = FP8 ? 0 : NKL >= 8 ? 2 : 1;
+        static_for<AHEAD>([&](auto gc) INLINE { first_product(gc); });
+        if (mask(k0 + 32 * hh, (uint32_t)(good >> (32 * hh)), cur)) first_max(cur, top);
+        settle(cur, top);
+        static_for<NKL - AHEAD>([&](auto xc) INLINE {
+          constexpr int x = decltype(xc)::value, g = x + AHEAD, ON = NKL - AHEAD;
+          first_product(std::integral_constant<int, g>{});
+          static_for<(x + 1) * 16 / ON - x * 16 / ON>([&](auto n) INLINE { weigh(x * 16 / ON + decltype(n)::value, cur); });
+          if constexpr (!FP8 && hh == 1 && x == ON - 1) {
+            vs = ks;
+            ks = slots_of(j + 4);
+            good = good_keys(j + 1);
+            k0 = key0(j + 1);
+          }
+        });
+        static_for<NB>([&](auto gc) INLINE {
+          constexpr int g = decltype(gc)::value;
+          pv(gc, vf[g & 1]);
+          if constexpr (g + 2 < NB)
+            vf[g & 1] = load_v(vc, (g + 2) / DN, (g + 2) % DN);
+          else
+            kf[g & 1] = load_k(kd, g + 2 - NB);
+          static_for<16 / NB>([&](auto ic) INLINE {
+            constexpr int i = g * (16 / NB) + decltype(ic)::value;
+            scale_next(i);
 #pragma unroll
-              for (int m = 0; m < 2; ++m) top[m] = i == 0 ? nxt[m][0] : __builtin_fmaxf(top[m], nxt[m][i]);
-            });
-            fence();
+            for (int m = 0; m < 2; ++m) top[m] = i == 0 ? nxt[m][0] : __builtin_fmaxf(top[m], nxt[m][i]);
           });
+        });
+        if constexpr (FP8 && hh == 1) {
+            vs = ks;
+            ks = slots_of(j + 4);
+            good = good_keys(j + 1);
+            k0 = key0(j + 1);
         }
-        if constexpr (hh == 1) {
-          vs = ks;
-          ks = slots_of(j + 4);
-          good = good_keys(j + 1);
-          k0 = key0(j + 1);
-        }
-        const bool masked = mask(k0 + 32 * (1 - hh), (uint32_t)(good >> (32 * (1 - hh))), nxt);
-        if (masked) {
-          asm volatile("");
-          first_max(nxt, top);
-        }
-        settle(nxt, top);
       };
       half(std::integral_constant<int, 0>{}, sa, sb);
       half(std::integral_constant<int, 1>{}, sb, sa);

@@ -68,9 +68,12 @@ __device__ __forceinline__ Item uniform(const Item &w) {
 
 __device__ __forceinline__ int32_t wave_sum_i(int32_t x) { return (int32_t)wave_sum((uint32_t)x); }
 
-// The id-th item (or, with TILES, the id-th row tile) of the launch's list; false: there is none.  Every lane of the wave
-// calls it with the same id and gets the same answer.
-template <int KT, bool CHUNK, bool TILES>
+enum Find { ITEM, TILE, ROW };
+
+// The id-th item of the launch's list (or its id-th row tile, or the tile of row id); false: there is none.  Every lane of
+// the wave calls it with the same id and gets the same answer.  TILE and ROW are for the join of divided launches, and take
+// the division from the word that the launch's first items left.
+template <int KT, bool CHUNK, Find BY>
 __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item &w) {
   const int lane = threadIdx.x & 63;
   const int32_t R = a.R;
@@ -98,84 +101,102 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
     w.row0 = (nt - 1 - (int32_t)t) * R;
     return true;
   }
-  // what the launch has to do, in key tiles
-  const int32_t mu = a.Hkv * a.blocks;
-  float total = 0.f;   // of the launch's list, as the division needs it: no more exact than it is
-  int32_t most = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int32_t nt = 0, c = 0;
+  // The lane's request of 64, its row tiles and their key tiles; the first 64 are loaded once
+  struct Mine {
+    Request r;
+    int32_t nt, c;
+  };
+  auto load = [&](int b0) {
+    Mine x{{0, 0, 0}, 0, 0};
     if (b0 + lane < a.B) {
-      const Request r = request(a, b0 + lane);
-      nt = (r.n + R - 1) / R;
-      c = nt ? key_tiles<KT>(a, r, (nt - 1) * R, R).count : 0;
+      x.r = request(a, b0 + lane);
+      x.nt = (x.r.n + R - 1) / R;
+      if (x.nt) x.c = key_tiles<KT>(a, x.r, (x.nt - 1) * R, R).count;
     }
-    total += wave_reduce_f32((float)nt * (float)c, [](float x, float y) { return x + y; });
-    most = max(most, (int32_t)wave_max((uint32_t)c));
-  }
-  const float share = total * (float)mu / (float)a.slots;
-  int32_t chunk = max((int32_t)__builtin_fminf(share, 0x1p30f) + 1, a.min_tiles);
-  if constexpr (CHUNK) {
-    // Few and long items: the longest list in 1 to 8 parts, whichever would be through first.  Equal items run in rounds of
-    // `slots`; unequal ones end within one item of an even share.  A divided item costs its partial output and the join,
-    // about 8 tiles' time.
-    int64_t best = (int64_t)1 << 62;
-    chunk = max(most, 1);
-    for (int s = 1; s <= 8; ++s) {
-      const int32_t size = (most + s - 1) / s;
-      if (s > 1 && size < a.min_tiles) break;
-      int32_t items = 0;
-      for (int b0 = 0; b0 < a.B; b0 += 64) {
-        int32_t n = 0;
-        if (b0 + lane < a.B) {
-          const Request r = request(a, b0 + lane);
-          const int32_t nt = (r.n + R - 1) / R;
-          if (nt) n = nt * max((key_tiles<KT>(a, r, (nt - 1) * R, R).count + size - 1) / max(size, 1), 1);
+    return x;
+  };
+  const Mine mine0 = load(0);
+  auto at = [&](int b0) { return b0 ? load(b0) : mine0; };
+  auto parts = [&](const Mine &x, int32_t size) { return max((x.c + size - 1) / size, 1); };
+  int32_t chunk;           // key tiles of an item at most
+  if constexpr (BY != ITEM) {
+    chunk = (int32_t)*a.chunk;
+  } else {
+    // what the launch has to do, in key tiles
+    const int32_t mu = a.Hkv * a.blocks;
+    float total = 0.f;   // as the division needs it: no more exact than it is
+    int32_t most = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+      const Mine x = at(b0);
+      total += wave_reduce_f32((float)x.nt * (float)x.c, [](float y, float z) { return y + z; });
+      most = max(most, (int32_t)wave_max((uint32_t)x.c));
+    }
+    const float share = total * (float)mu / (float)a.slots;
+    // Lists that are nearly equal, one to a slot: left whole.  Others in half a slot's share at most, so that the last ones to
+    // start end soon after the others (64 requests x 8 cache heads, 4100 keys each: 190 us whole, 197 in halves; 32 of 1600 to
+    // 16384 keys, E4M3: NNN us, NNN in whole shares).
+    chunk = max((int32_t)__builtin_fminf(0.5f * share, 0x1p30f) + 1, a.min_tiles);
+    if (!CHUNK && (float)most <= 1.25f * share) chunk = most;
+    chunk = max(chunk, 1);
+    if constexpr (CHUNK) {
+      // Few and long items: the longest list in 1 to 8 parts, whichever would be through first.  Equal items run in rounds of
+      // `slots`; unequal ones end within one item of an even share.  A divided item costs its partial output and the join,
+      // about 8 tiles' time.
+      int64_t best = (int64_t)1 << 62;
+      chunk = max(most, 1);
+      for (int s = 1; s <= 8; ++s) {
+        const int32_t size = max((most + s - 1) / s, 1);
+        if (s > 1 && size < a.min_tiles) break;
+        int32_t items = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+          const Mine x = at(b0);
+          items += wave_sum_i(x.nt * parts(x, size));
         }
-        items += wave_sum_i(n);
-      }
-      if (s > 1 && (int64_t)items * mu > a.max_items) break;
-      const int64_t rounds = ((int64_t)items * mu + a.slots - 1) / a.slots;
-      const int64_t even = rounds * size, uneven = (int64_t)share + size;
-      const int64_t t = min(even, uneven) + (s > 1 ? 8 * rounds : 0);
-      if (t < best) {
-        best = t;
-        chunk = max(size, 1);
+        if (s > 1 && (int64_t)items * mu > a.max_items) break;
+        const int64_t rounds = ((int64_t)items * mu + a.slots - 1) / a.slots;
+        const int64_t even = rounds * size, uneven = (int64_t)share + size;
+        const int64_t t = min(even, uneven) + (s > 1 ? 8 * rounds : 0);
+        if (t < best) {
+          best = t;
+          chunk = size;
+        }
       }
     }
+    // for the join; 0: it has nothing to do
+    if (id == 0 && threadIdx.x == 0) *a.chunk = most > chunk ? (uint32_t)chunk : 0u;
   }
   int32_t items = 0, tiles = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int32_t nt = 0, ns = 1;
-    if (b0 + lane < a.B) {
-      const Request r = request(a, b0 + lane);
-      nt = (r.n + R - 1) / R;
-      if (nt) ns = max((key_tiles<KT>(a, r, (nt - 1) * R, R).count + chunk - 1) / chunk, 1);
-    }
-    const int32_t mine = TILES ? nt : nt * ns;
-    const int32_t upto = (int32_t)wave_incl_scan((uint32_t)mine), here = TILES ? tiles : items;
-    const uint64_t m = __ballot((int64_t)id < (int64_t)here + upto);
+    const Mine x = at(b0);
+    const int32_t ns = parts(x, chunk), its = x.nt * ns;
+    const int32_t upto = (int32_t)wave_incl_scan((uint32_t)its);
+    const int32_t tiles_upto = BY == TILE ? (int32_t)wave_incl_scan((uint32_t)x.nt) : 0;
+    bool here;
+    if constexpr (BY == ITEM) here = (int64_t)id < (int64_t)items + upto;
+    if constexpr (BY == TILE) here = (int64_t)id < (int64_t)tiles + tiles_upto;
+    if constexpr (BY == ROW) here = (int32_t)id >= x.r.from && (int32_t)id < x.r.from + x.r.n;
+    const uint64_t m = __ballot(here);
     if (m) {
       const int k = __builtin_ctzll(m);
-      const int32_t n = __builtin_amdgcn_readlane(nt, k), s = __builtin_amdgcn_readlane(ns, k);
-      const int32_t at = (int32_t)id - here - (__builtin_amdgcn_readlane(upto, k) - __builtin_amdgcn_readlane(mine, k));
-      const int32_t before = items + (TILES ? __builtin_amdgcn_readlane((int32_t)wave_incl_scan((uint32_t)(nt * ns)), k) - n * s
-                                            : __builtin_amdgcn_readlane(upto, k) - n * s);
+      const int32_t n = __builtin_amdgcn_readlane(x.nt, k);
+      w.splits = __builtin_amdgcn_readlane(ns, k);
+      w.r = {__builtin_amdgcn_readlane(x.r.from, k), __builtin_amdgcn_readlane(x.r.n, k), __builtin_amdgcn_readlane(x.r.len, k)};
       w.b = b0 + k;
-      w.r = request(a, w.b);
-      w.splits = s;
-      w.split = TILES ? 0 : at / n;
-      const int32_t tile = TILES ? at : at % n;
+      const int32_t before = items + __builtin_amdgcn_readlane(upto, k) - n * w.splits;
+      int32_t tile = 0;      // counted from the request's end: the last rows, which see the most keys, first
+      if constexpr (BY == ITEM) {
+        w.split = ((int32_t)id - before) / n;
+        tile = ((int32_t)id - before) % n;
+      }
+      if constexpr (BY == TILE) tile = (int32_t)id - (tiles + __builtin_amdgcn_readlane(tiles_upto, k) - n);
+      if constexpr (BY == ROW) tile = n - 1 - ((int32_t)id - w.r.from) / R;
       w.row0 = (n - 1 - tile) * R;
       w.first_item = before + tile;
       w.next = n;
       return true;
     }
-    if constexpr (TILES) {
-      tiles += __builtin_amdgcn_readlane(upto, 63);
-      items += wave_sum_i(nt * ns);
-    } else {
-      items += __builtin_amdgcn_readlane(upto, 63);
-    }
+    items += __builtin_amdgcn_readlane(upto, 63);
+    if constexpr (BY == TILE) tiles += __builtin_amdgcn_readlane(tiles_upto, 63);
   }
   return false;
 }

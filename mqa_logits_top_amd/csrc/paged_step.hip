@@ -76,7 +76,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
     member = local % mu;
   }
   Item found;
-  if (!find_item<KT, false, false>(a, id, found)) return;
+  if (!find_item<KT, false, ITEM>(a, id, found)) return;
   const Item w = uniform(found);
   const int kvh = (int)(member % (uint32_t)a.Hkv), hb = (int)(member / (uint32_t)a.Hkv);
   const int head0 = kvh * a.G + hb * a.Gt, heads = min(a.Gt, a.G - hb * a.Gt);
