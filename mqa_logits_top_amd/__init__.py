@@ -864,9 +864,15 @@ def idx_paged_attn(q: torch.Tensor, k: Cache, v: Cache, pages: torch.Tensor, cu_
 
 def _norm_rows(x: torch.Tensor, what: str) -> idx_rows:
     """Rows [T, H, D], or hidden rows [T, D] as one head."""
-    if x.dim() == 2:
-        x = x.unsqueeze(1)
-    return _rows(x, what)
+    if x.dim() != 2:
+        return _rows(x, what)
+    if x.requires_grad and torch.is_grad_enabled():
+        return _rows(x.unsqueeze(1), what)          # refuses them
+    dtype, (T, D), ld = _VALUE.get(x.dtype), x.shape, x.stride()
+    if dtype is None or not x.is_cuda or (ld[1] != 1 and D > 1):
+        raise ValueError(f"{what}: [T, D] or [T, H, D] bfloat16, float16 or float32 on the GPU with a contiguous last "
+                         f"dimension, got {[T, D]} {x.dtype} on {x.device}, strides {ld}")
+    return idx_rows(x.data_ptr(), ld[0], D, dtype, T, 1, D)
 
 
 def idx_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -876,43 +882,42 @@ def idx_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
     with_out is False).  residual: added before the norm, the sum written to `total`, or to the residual itself where that
     is None.  to: an E4M3 cache of T slots or more that receives the result with a scale for each of its heads, which for
     x [T, D] may be groups of D."""
-    rows, device = _norm_rows(x, "x"), x.device
-    none = idx_rows()
-    r = t = none
+    rows, device, shape = _norm_rows(x, "x"), x.device, x.shape
+    n = idx_norm()
+    n.x, n.eps, n.weight_dtype = rows, eps, IDX_K_F32
     if residual is not None:
-        total = residual if total is None else total
-        if residual.shape != x.shape or total.shape != x.shape:
-            raise ValueError(f"residual and total: {list(x.shape)} as x, got {list(residual.shape)} and {list(total.shape)}")
-        if residual.device != device or total.device != device:
-            raise ValueError(f"residual on {residual.device} and total on {total.device} for x on {device}")
-        r, t = _norm_rows(residual, "residual"), _norm_rows(total, "total")
+        if residual.shape != shape or residual.device != device:
+            raise ValueError(f"residual: {list(shape)} on {device} as x, got {list(residual.shape)} on {residual.device}")
+        n.residual = r = _norm_rows(residual, "residual")
+        if total is None or total is residual:
+            n.total = r
+        elif total.shape != shape or total.device != device:
+            raise ValueError(f"total: {list(shape)} on {device} as x, got {list(total.shape)} on {total.device}")
+        else:
+            n.total = _norm_rows(total, "total")
     elif total is not None:
         raise ValueError("total without a residual")
-    w, w_type = None, IDX_K_F32
     if weight is not None:
         if weight.requires_grad and torch.is_grad_enabled():
             raise ValueError("weight requires a gradient, and no entry point records one: call it under torch.no_grad() "
                              "or on weight.detach()")
-        if weight.shape != x.shape[-1:] or weight.dtype not in _VALUE:
-            raise ValueError(f"weight: {list(x.shape[-1:])} bfloat16, float16 or float32, got {list(weight.shape)} "
+        if weight.shape != shape[-1:] or weight.dtype not in _VALUE:
+            raise ValueError(f"weight: {list(shape[-1:])} bfloat16, float16 or float32, got {list(weight.shape)} "
                              f"{weight.dtype}")
-        w, w_type = _on(weight, device, weight.dtype, "weight"), _VALUE[weight.dtype]
-    codes = None
+        n.weight, n.weight_dtype = _on(weight, device, weight.dtype, "weight"), _VALUE[weight.dtype]
     if to is not None:
         if to.device != device:
             raise ValueError(f"a cache on {to.device} for x on {device}")
-        codes = ctypes.pointer(to._struct)
+        n.to = ctypes.pointer(to._struct)
     with _on_stream(device, stream) as st:
         if out is not None:
-            if out.device != device or out.shape != x.shape:
-                raise ValueError(f"out: {list(x.shape)} on {device}, got {list(out.shape)} on {out.device}")
-            o = _norm_rows(out, "out")
+            if out.device != device or out.shape != shape:
+                raise ValueError(f"out: {list(shape)} on {device}, got {list(out.shape)} on {out.device}")
+            n.out = _norm_rows(out, "out")
         elif with_out:
-            out = x.new_empty(x.shape)
-            o = _new_rows(out, rows.dtype, rows.T, rows.H, rows.D)
-        else:
-            o = none
-        s = load_library().idx_rms_norm(idx_norm(rows, r, t, o, codes, w, w_type, eps), st)
+            out = x.new_empty(shape)
+            n.out = _new_rows(out, rows.dtype, rows.T, rows.H, rows.D)
+        s = load_library().idx_rms_norm(n, st)
     if s:
         raise IdxError("idx_rms_norm", s)
     return out

@@ -187,6 +187,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
 #pragma unroll
     for (int d = 0; d < DN; ++d) o[m][d] = f32x16{};
 
+  // Q^T as B operands: lane l holds row l % 32 and 8 dims of each 16
+  u32x4 q[2][KS];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const Row r = row_of(m);
+    const uint8_t *at = a.q + (r.real ? (int64_t)r.t * a.q_t + (int64_t)r.h * a.q_h : 0);
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      const int e = FP8 ? 32 * (s >> 1) + 16 * hl + 8 * (s & 1) : 16 * s + 8 * hl;
+      q[m][s] = *(const u32x4 *)(at + 2 * e);   // rows that are not there: any row's, masked and not stored
+    }
+  }
+
   Slots ks, vs;       // of K(j + 3) and V(j + 2) in step j
   if (nv > 0) {
 #pragma unroll
@@ -287,18 +300,6 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       vst = vst == 2 ? 0 : vst + 1;
     }
   } else if (nv > 0) {
-    // Q^T as B operands: lane l holds row l % 32 and 8 dims of each 16
-    u32x4 q[2][KS];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const Row r = row_of(m);
-      const uint8_t *at = a.q + (r.real ? (int64_t)r.t * a.q_t + (int64_t)r.h * a.q_h : 0);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const int e = FP8 ? 32 * (s >> 1) + 16 * hl + 8 * (s & 1) : 16 * s + 8 * hl;
-        q[m][s] = *(const u32x4 *)(at + 2 * e);   // rows that are not there: any row's, masked and not stored
-      }
-    }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -337,15 +338,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     auto mask = [&](int32_t k0, uint32_t good, f32x16 *s) INLINE -> bool {
       if ((uint32_t)k0 - whole0 <= whole_span && good == ~0u) return false;
       asm volatile("");   // stays a branch
-      const uint32_t mine = good >> (4 * hl);
+      // a bit for each key that the row sees
+      auto below = [&](int32_t key) INLINE -> uint32_t {   // of the 32 keys from k0 on
+        return key <= k0 ? 0u : key - k0 >= 32 ? ~0u : (1u << (key - k0)) - 1u;
+      };
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int off = 8 * (i / 4) + i % 4;
-        const int32_t key = k0 + off + 4 * hl;
+      for (int m = 0; m < 2; ++m) {
+        const uint32_t sees = (below(pos[m] + 1) & (~below(lb[m] + 1) | below(a.first)) & good) >> (4 * hl);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const bool sees = (key <= pos[m]) & ((key > lb[m]) | (key < a.first)) & ((mine >> off) & 1u);
-          s[m][i] = sees ? s[m][i] : NEG_INF;
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t keep = (uint32_t)((int32_t)(sees << (31 - (8 * (i / 4) + i % 4))) >> 31);
+          s[m][i] = __uint_as_float((__float_as_uint(s[m][i]) & keep) | (0xFF800000u & ~keep));
         }
       }
       return true;
@@ -562,6 +565,17 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   }
   copies_left<0>();   // none may write LDS that is another workgroup's by then
 
+  // whether any wave left some values out; and the others have read their last tile
+  constexpr int OUT_CH = D / 8;   // 16-byte chunks of a row of out
+  uint8_t *const mine = lds + wave * 64 * 2 * D;
+  uint32_t *const word = (uint32_t *)(lds + M * 2 * D);
+  static_assert(M * 2 * D + 4 * WAVES <= chunk_lds<FP8, D>(), "the output fits");
+  if (nv > 0) {
+    __syncthreads();
+    if (lane == 0) word[wave] = odd_seen;
+    __syncthreads();
+    odd_seen = (word[0] | word[1] | word[2] | word[3]) != 0u;
+  }
   // lane l holds row l % 32 and dims 32 d + 8 (z / 4) + 4 (l / 32) + z % 4
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
@@ -580,24 +594,24 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
               f32x4{o[m][d][z], o[m][d][z + 1], o[m][d][z + 2], o[m][d][z + 3]};
     } else {
       const float f = finish(l);
-      uint8_t *dst = a.out + (int64_t)r.t * a.out_t + (int64_t)r.h * a.out_h;
 #pragma unroll
       for (int d = 0; d < DN; ++d)
 #pragma unroll
         for (int z = 0; z < 16; z += 4)
-          *(uint2 *)(dst + 2 * (32 * d + 2 * z + 4 * hl)) =
+          *(uint2 *)(mine + (m * 32 + c) * 2 * D + (((4 * d + z / 4) ^ (c & (OUT_CH - 1))) << 4) + 8 * hl) =
               make_uint2(pack2<BF16>(o[m][d][z] * f, o[m][d][z + 1] * f), pack2<BF16>(o[m][d][z + 2] * f, o[m][d][z + 3] * f));
       if (hl == 0 && a.lse) a.lse[(int64_t)r.t * a.Hq + r.h] = lse_of(ref[m], l);
     }
   }
-  if (nv > 0) {   // whether any wave left some out
-    uint32_t *const word = (uint32_t *)lds;
-    __syncthreads();
-    if (threadIdx.x == 0) *word = 0u;
-    __syncthreads();
-    if (odd_seen && lane == 0) *word = 1u;
-    __syncthreads();
-    odd_seen = *word != 0u;
+  if (w.splits == 1) {   // through LDS, so that whole rows are stored at a time
+    wave_sync();
+    for (int i = 0; i < OUT_CH; ++i) {
+      const int x = i * (64 / OUT_CH) + lane / OUT_CH, ch = lane & (OUT_CH - 1);
+      const int row = wave * 64 + x, tok = row / a.Gt, h = row - tok * a.Gt;
+      if (tok < a.R && h < heads && w.row0 + tok < w.r.n)
+        *(u32x4 *)(a.out + (int64_t)(w.r.from + w.row0 + tok) * a.out_t + (int64_t)(head0 + h) * a.out_h + 16 * ch) =
+            *(const u32x4 *)(mine + x * 2 * D + ((ch ^ (x & (OUT_CH - 1))) << 4));
+    }
   }
   if (odd_seen) {
     asm volatile("");   // stays a branch
