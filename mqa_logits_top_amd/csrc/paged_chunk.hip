@@ -158,10 +158,13 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     v_off[u] = (uint32_t)(((lane & (CH - 1)) ^ swizzle_v(r)) << 4) + (RUNS ? (uint32_t)r * a.row_bytes : 0u);
   }
   auto request = [&](const uint8_t *base, const Slots &s, uint32_t off, int u, uint32_t at) INLINE {
-    if constexpr (RUNS)
+    if constexpr (RUNS) {
       copy16(uniform(base + s), off, at);
-    else
-      copy16(base, (uint64_t)s[u] * a.row_bytes + off, at);
+    } else {
+      uint64_t x = (uint64_t)s[u] * a.row_bytes + off;
+      asm volatile("" : "+v"(x));   // the base is added here; added to every offset before the loop it fills registers
+      copy16(base, x, at);
+    }
   };
   auto request_k = [&](int stage, const Slots &s, int u) INLINE {
     request(kbase, s, k_off[u], u, lds_addr(lds + stage * KV + (16 * wave + u * RPC) * RB));
@@ -433,17 +436,20 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       }
     };
     u32x4 p[2][2], rest[2][2];   // weights of 16 keys each, and their second parts
-    f32x4 vsc[4];
+    f32x4 vsc;   // E4M3: scales of the values of four keys
     // Weights of two keys, the n-th pair of the 16: keys in the order of the second product's steps
-    auto weigh = [&](int n, const f32x16 *s) INLINE {
+    auto weigh = [&](int n, const f32x16 *s, int v, int half) INLINE {
       const int m = n & 1, i = n >> 1 << 1;
+      if constexpr (FP8) {
+        if (n % 4 == 0) vsc = scales_at(v, half, i / 4, 1);
+      }
       float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i], a.scale2, nb[m]));
       float y = __builtin_amdgcn_exp2f(__builtin_fmaf(s[m][i + 1], a.scale2, nb[m]));
       sum[m] += x;
       sum[m] += y;
       if constexpr (FP8) {
-        x *= vsc[i / 4][i % 4];
-        y *= vsc[i / 4][i % 4 + 1];
+        x *= vsc[i % 4];
+        y *= vsc[i % 4 + 1];
       }
       uint32_t b = pack2<PV_BF16>(x, y);
       if constexpr (TWO) {
@@ -491,10 +497,6 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         constexpr int hh = decltype(hc)::value;
         constexpr int NB = 2 * DN;
         const uint32_t kc = hh == 0 ? kp + 32 * RB : kn, kd = hh == 0 ? kn : kn + 32 * RB, vc = vp + hh * 32 * RB;
-        if constexpr (FP8) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) vsc[x] = scales_at(j, hh, x, 1);
-        }
         auto copies = [&](auto gc) INLINE {   // one load's share of the step's
           constexpr int g = decltype(gc)::value;
           if constexpr (hh == 0) {
@@ -529,7 +531,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         static_for<NKL - AHEAD>([&](auto xc) INLINE {
           constexpr int x = decltype(xc)::value, g = x + AHEAD, ON = NKL - AHEAD;
           first_product(std::integral_constant<int, g>{});
-          static_for<(x + 1) * 16 / ON - x * 16 / ON>([&](auto n) INLINE { weigh(x * 16 / ON + decltype(n)::value, cur); });
+          static_for<(x + 1) * 16 / ON - x * 16 / ON>([&](auto n) INLINE { weigh(x * 16 / ON + decltype(n)::value, cur, j, hh); });
           if constexpr (!FP8 && hh == 1 && x == ON - 1) {
             vs = ks;
             ks = slots_of(j + 4);

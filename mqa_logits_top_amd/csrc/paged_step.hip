@@ -48,7 +48,7 @@ constexpr int step_lds() {
 
 // RUNS: pages of 16 slots and more, and a cache of whole pages.
 template <bool BF16, bool FP8, int D, int MT, bool RUNS>
-__global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
+__global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? (RUNS && BF16 ? 4 : 3) : 2) void step_kernel(PagedArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
   constexpr bool TWO = FP8 && !BF16;      // ... and, for fp16 results, two parts
   constexpr float LIFT = !PV_BF16 ? 7.f : 0.f;
@@ -165,20 +165,26 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
     }
     return x;
   };
-  uint32_t k_off[NI], v_off[NI];   // of the lane's chunk: with RUNS also of its row in the run
+  // offsets of the lane's chunks: with RUNS also of its row in the run, else one, from which the others are an exclusive or
+  // away (a swizzle's bits are bits of the row's number)
+  constexpr int NO = RUNS ? NI : 1;
+  uint32_t k_off[NO], v_off[NO];
 #pragma unroll
-  for (int u = 0; u < NI; ++u) {
+  for (int u = 0; u < NO; ++u) {
     const int r = u * RPC + my_row;
     k_off[u] = (uint32_t)(((lane & (CH - 1)) ^ swizzle_k(r)) << 4) + (RUNS ? (uint32_t)(r & 15) * a.row_bytes : 0u);
     v_off[u] = (uint32_t)(((lane & (CH - 1)) ^ swizzle_v(r)) << 4) + (RUNS ? (uint32_t)(r & 15) * a.row_bytes : 0u);
   }
-  auto request = [&](const uint8_t *base, const Slots &x, const uint32_t *off, uint8_t *to) INLINE {
+  auto request = [&](const uint8_t *base, const Slots &x, const uint32_t *off, auto swizzle, uint8_t *to) INLINE {
 #pragma unroll
     for (int u = 0; u < NI; ++u) {
-      if constexpr (RUNS)
+      if constexpr (RUNS) {
         copy16(uniform(base + (uint64_t)x.s[u * RPC / 16] * a.row_bytes), off[u], lds_addr(to) + u * 1024);
-      else
-        copy16(base, (uint64_t)x.s[u] * a.row_bytes + off[u], lds_addr(to) + u * 1024);
+      } else {
+        uint64_t at = (uint64_t)x.s[u] * a.row_bytes + (off[0] ^ (uint32_t)(swizzle(u * RPC) << 4));
+        asm volatile("" : "+v"(at));   // the base is added here; added to every offset before the loop it fills registers
+        copy16(base, at, lds_addr(to) + u * 1024);
+      }
     }
   };
   // lanes 0 .. 31 bring their key's scale, the others their value's
@@ -186,7 +192,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
     if constexpr (FP8) {
       uint32_t s;
       if constexpr (RUNS) {
-        s = (lane & 16 ? x.s[1] : x.s[0]) + (uint32_t)(lane & 15);
+        const uint32_t other = -(uint32_t)((lane >> 4) & 1);   // (a choice of the two would go through memory)
+        s = (x.s[0] ^ ((x.s[0] ^ x.s[1]) & other)) + (uint32_t)(lane & 15);
       } else {
         bool ok;
         s = slot_of(ids[(j & (IDS - 1)) * 64 + (lane & 31)], min(key0(j) + (lane & 31), last_key), ok);
@@ -213,8 +220,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
     Slots slots = slots_of(0);
     uint32_t good_now = good;
     request_scales(0, slots);
-    request(kbase, slots, k_off, kbuf);
-    request(vbase, slots, v_off, vbuf);
+    request(kbase, slots, k_off, swizzle_k, kbuf);
+    request(vbase, slots, v_off, swizzle_v, vbuf);
     // Q^T as B operands: lane l holds row l % 16 and the dims its K piece holds in that step
     u32x4 q[MT][KS];
 #pragma unroll
@@ -260,7 +267,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
       // behind the last tile it is requested once more and not used: the waits count on it
       request_ids(j + 2);
       request_scales(j + 1, next);
-      request(kbase, next, k_off, kbuf);
+      request(kbase, next, k_off, swizzle_k, kbuf);
       if constexpr (FP8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -438,7 +445,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void step_kernel(PagedArgs a) {
           lds_done();
         }
       }
-      request(vbase, next, v_off, vbuf);
+      request(vbase, next, v_off, swizzle_v, vbuf);
       good_now = good;
       if constexpr (FP8) {
 #pragma unroll
