@@ -479,7 +479,8 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
  * The sums are divided last: values within a factor of 2^8 len_k of fp32's largest number can overflow them.
  * A call's results are bitwise repeatable; a row's bits depend on the sizes and lengths of the call, by which its keys
  * are divided, and not on what other rows hold.
- * page: a power of two; n_pages * page below 2^31; B up to 2^16; T * Hq below 2^26.
+ * page: a power of two; n_pages * page below 2^31; B up to 2^16; T * Hq below 2^26; B * k.H, and the row tiles of a call
+ * (T * Hq / 256 + B * k.H, about), below 2^23.
  * ws: idx_paged_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap in time need one
  * each. */
 typedef struct idx_paged {
@@ -510,7 +511,8 @@ idx_status idx_paged_attn(const idx_paged *a, void *ws, size_t ws_bytes, void *s
  * total is not read.  out.data NULL: codes only; to NULL: values only; one of them is given.  total may be residual or x
  * itself, and out may be x, residual (with another total) or, for codes only, absent; in place the strides are the same.
  * Otherwise outputs share no byte with inputs or with each other.
- * D a multiple of 8, at most 32768; groups smaller than a row are 8, 16, 32, ... 512 values; T * H below 2^31 / 64. */
+ * D a multiple of 8, at most 32768; groups smaller than a row are 8, 16, 32, ... 512 values; T * H times
+ * the power of two at or above D / 8 below 2^31. */
 typedef struct idx_norm {
   idx_rows x, residual, total, out;
   const idx_cache *to;          /* nullable; read during the call only */

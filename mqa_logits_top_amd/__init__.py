@@ -822,6 +822,8 @@ def idx_paged_attn(q: torch.Tensor, k: Cache, v: Cache, pages: torch.Tensor, cu_
             or (pages.stride(1) != 1 and pages.shape[1] > 1)):
         raise ValueError(f"pages: [B, n] int32 on {device} with a contiguous last dimension, got {list(pages.shape)} "
                          f"{pages.dtype} on {pages.device}")
+    if not (0 <= page < 1 << 31 and 0 <= window < 1 << 31 and 0 <= first < 1 << 31):
+        raise ValueError(f"page, window and first from 0 to 2^31 - 1, got {page}, {window}, {first}")
     B = pages.shape[0]
     if cu_q.shape != (B + 1,) or len_k.shape != (B,):
         raise ValueError(f"cu_q: [{B + 1}] and len_k: [{B}] for {B} rows of pages, got {list(cu_q.shape)} and "

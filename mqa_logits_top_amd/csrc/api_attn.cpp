@@ -168,6 +168,10 @@ idx_status check_attn(const idx_attn *a) {
   return IDX_OK;
 }
 
+idx::PagedPlan plan_of(const idx_paged *a) {
+  return idx::plan_paged(a->q.T, a->B, a->k.H, a->q.H / a->k.H, a->q.D, a->n_pages * a->page);
+}
+
 idx_status check_paged(const idx_paged *a) {
   if (!a) return IDX_E_NULL;
   const idx_status st = check_attn_arrays(a);
@@ -180,12 +184,8 @@ idx_status check_paged(const idx_paged *a) {
   if (a->window < 0 || a->first < 0) return IDX_E_PARAM;
   if (a->q.T > 0 && a->B > 0 && (!a->cu_q || !a->len_k || (a->n_pages > 0 && !a->pages))) return IDX_E_NULL;
   if (!aligned(a->pages, 4) || !aligned(a->cu_q, 4) || !aligned(a->len_k, 4)) return IDX_E_ALIGN;
-  return IDX_OK;
-}
-
-idx::PagedPlan plan_of(const idx_paged *a) {
-  return idx::plan_paged(a->q.T, a->B, a->k.H, a->q.H / a->k.H, a->q.D, a->k.fmt == IDX_K_FP8_E4M3,
-                         a->n_pages * a->page);
+  // workgroups of 256 lanes, fewer than 2^32 lanes
+  return plan_of(a).max_items < (int64_t)1 << 23 ? IDX_OK : IDX_E_UNSUPPORTED;
 }
 
 // Whether two row arrays that start together lie alike; true where they do not.
@@ -204,7 +204,7 @@ idx_status check_norm(const idx_norm *n) {
   if (n->weight && (!value_type(n->weight_dtype))) return IDX_E_FORMAT;
   if (!aligned(n->weight, 16)) return IDX_E_ALIGN;
   if (x.T == 0 || x.H == 0) return IDX_OK;
-  if ((int64_t)x.T * x.H >= MAX_LANES / 64) return IDX_E_UNSUPPORTED;
+  if (lanes_of(x) >= MAX_LANES) return IDX_E_UNSUPPORTED;
   if (!n->out.data && !n->to) return IDX_E_NULL;
   if (n->residual.data) {
     if ((st = check_rows(n->residual, false, MAX_NORM)) || (st = check_rows(n->total, true, MAX_NORM))) return st;

@@ -38,6 +38,11 @@ struct PagedArgs {
   uint32_t *chunk;           // the division, for the join (0: nothing is divided)
 };
 
+// Whether the 16 keys from a multiple of 16 on follow each other in the caches, within a 32-bit offset.
+inline bool has_runs(const PagedArgs &a) {
+  return a.page_sh >= 4 && a.rows >> a.page_sh << a.page_sh == a.rows && (uint64_t)a.row_bytes * 16 < (1ull << 32);
+}
+
 struct PagedPlan {
   bool chunk;                // paged_chunk.hip, else paged_step.hip
   int32_t M;                 // rows (tokens x heads) of a workgroup
@@ -47,7 +52,7 @@ struct PagedPlan {
   int64_t max_items;
   size_t bytes;              // workspace
 };
-PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len);
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len);
 hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
                         hipStream_t s);
 hipError_t launch_paged_chunk(const PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, hipStream_t s);

@@ -124,7 +124,7 @@ __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
 
 }  // namespace
 
-PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bool fp8, int32_t max_len) {
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len) {
   PagedPlan p{};
   const int32_t live = B < T ? (B > 0 ? B : 1) : (T > 0 ? T : 1);   // requests that can have rows
   const int64_t need = (int64_t)((T + live - 1) / live) * G;        // rows of a request and cache head, about
@@ -153,7 +153,6 @@ PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, bo
 hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
                         hipStream_t s) {
   if (plan.max_items <= 0) return hipSuccess;
-  if (plan.max_items > INT32_MAX / 32) return hipErrorInvalidValue;
   if (a.rows == 0) a.max_len = 0;   // no slot that could be read
   // a negative factor turns q over instead, so that the largest product comes from the largest dot
   a.q_sign = a.scale2 < 0.f ? 0x80008000u : 0u;

@@ -45,8 +45,8 @@ constexpr int chunk_lds() {
   return (KSTAGES + VSTAGES) * KT * (FP8 ? D : 2 * D) + WAVES * IDS * KT * 4 + (FP8 ? KSTAGES * WAVES * 256 : 0);
 }
 
-// RUNS: pages of 16 slots and more, and a cache of whole pages: the 16 keys of a tile that a wave brings follow each other
-// in a cache, and their copies have one scalar address.
+// RUNS (has_runs): the 16 keys of a tile that a wave brings follow each other in a cache, and their copies have one scalar
+// address.
 template <bool BF16, bool FP8, int D, bool RUNS>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(PagedArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
@@ -585,8 +585,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     const Row r = row_of(m);
     if (!r.real) continue;
     if (w.splits > 1) {
-      const int64_t item = (int64_t)(w.first_item + w.split * w.next) * mu + member;
-      const int64_t at = item * M + wave * 64 + m * 32 + c;
+      const int64_t at = (int64_t)blockIdx.x * M + wave * 64 + m * 32 + c;
       if (hl == 0) *(float2 *)(a.part_ml + 2 * at) = make_float2(ref[m], l);
 #pragma unroll
       for (int d = 0; d < DN; ++d)
@@ -650,7 +649,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           for (int e = 0; e < E; ++e) {
             if (!odd[e]) continue;
             if (w.splits > 1) {
-              float *to = a.part + (((int64_t)(w.first_item + w.split * w.next) * mu + member) * M + row) * D + lane * E + e;
+              float *to = a.part + ((int64_t)blockIdx.x * M + row) * D + lane * E + e;
               *to += val[e];
             } else {
               uint16_t *to = (uint16_t *)(a.out + tq * a.out_t + (int64_t)(head0 + h) * a.out_h) + lane * E + e;
@@ -669,7 +668,7 @@ template <bool BF16, bool FP8, int D>
 hipError_t launch_one(const PagedArgs &a, hipStream_t s) {
   const dim3 grid((unsigned)a.max_items), block(64 * WAVES);
   constexpr int lds = chunk_lds<FP8, D>();
-  if (a.page_sh >= 4 && a.rows >> a.page_sh << a.page_sh == a.rows)
+  if (has_runs(a))
     hipLaunchKernelGGL((chunk_kernel<BF16, FP8, D, true>), grid, block, lds, s, a);
   else
     hipLaunchKernelGGL((chunk_kernel<BF16, FP8, D, false>), grid, block, lds, s, a);

@@ -133,8 +133,8 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
     }
     const float share = total * (float)mu / (float)a.slots;
     // Lists that are nearly equal, one to a slot: left whole.  Others in half a slot's share at most, so that the last ones to
-    // start end soon after the others (64 requests x 8 cache heads, 4100 keys each: 190 us whole, 197 in halves; 32 of 1600 to
-    // 16384 keys, E4M3: NNN us, NNN in whole shares).
+    // start end soon after the others (64 requests x 8 cache heads, 4100 keys each: 192 us whole, 203 in halves; 32 of 1600 to
+    // 16384 keys, E4M3: 161 us in halves, 187 in whole shares).
     chunk = max((int32_t)__builtin_fminf(0.5f * share, 0x1p30f) + 1, a.min_tiles);
     if (!CHUNK && (float)most <= 1.25f * share) chunk = most;
     chunk = max(chunk, 1);
@@ -185,15 +185,17 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
       const int32_t before = items + __builtin_amdgcn_readlane(upto, k) - n * w.splits;
       int32_t tile = 0;      // counted from the request's end: the last rows, which see the most keys, first
       if constexpr (BY == ITEM) {
-        w.split = ((int32_t)id - before) / n;
-        tile = ((int32_t)id - before) % n;
+        w.split = n > 0 ? ((int32_t)id - before) / n : 0;
+        tile = n > 0 ? ((int32_t)id - before) % n : 0;
       }
       if constexpr (BY == TILE) tile = (int32_t)id - (tiles + __builtin_amdgcn_readlane(tiles_upto, k) - n);
       if constexpr (BY == ROW) tile = n - 1 - ((int32_t)id - w.r.from) / R;
+      // (bounds that are not ascending could count past 32 bits, or past the launch)
+      if (n <= 0 || tile < 0 || tile >= n || w.split < 0 || w.split >= w.splits) return false;
       w.row0 = (n - 1 - tile) * R;
       w.first_item = before + tile;
       w.next = n;
-      return true;
+      return BY == ITEM || (w.first_item >= 0 && ((int64_t)w.first_item + (int64_t)(w.splits - 1) * n + 1) * a.Hkv * a.blocks <= a.max_items);
     }
     items += __builtin_amdgcn_readlane(upto, 63);
     if constexpr (BY == TILE) tiles += __builtin_amdgcn_readlane(tiles_upto, 63);

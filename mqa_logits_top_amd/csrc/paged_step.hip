@@ -46,7 +46,7 @@ constexpr int step_lds() {
   return WAVES * step_wave_lds<FP8, D, MT>() + WAVES * MT * 16 * 8;
 }
 
-// RUNS: pages of 16 slots and more, and a cache of whole pages.
+// RUNS: has_runs.
 template <bool BF16, bool FP8, int D, int MT, bool RUNS>
 __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? (RUNS && BF16 ? 4 : 3) : 2) void step_kernel(PagedArgs a) {
   constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
@@ -493,7 +493,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? (RUNS && BF16 ? 4 : 3)
     }
     const int64_t t = w.r.from + w.row0 + tok, hq = head0 + h;
     if (w.splits > 1) {
-      const int64_t at = ((int64_t)(w.first_item + w.split * w.next) * mu + member) * M + row;
+      const int64_t at = ((int64_t)id * mu + member) * M + row;
       *(f32x4 *)(a.part + at * D + 4 * y) = r;
       if (y == 0) *(float2 *)(a.part_ml + 2 * at) = make_float2(top, total);
     } else {
@@ -510,7 +510,7 @@ hipError_t launch_tiles(const PagedArgs &a, hipStream_t s) {
   const int64_t mu = (int64_t)a.Hkv * a.blocks;
   const int64_t grid = FP8 ? (a.max_items / mu + 8) / 8 * 8 * mu : a.max_items;
   constexpr int lds = step_lds<FP8, D, MT>();
-  if (a.page_sh >= 4 && a.rows >> a.page_sh << a.page_sh == a.rows)
+  if (has_runs(a))
     hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, true>), dim3((unsigned)grid), dim3(64 * WAVES), lds, s, a);
   else
     hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, false>), dim3((unsigned)grid), dim3(64 * WAVES), lds, s, a);

@@ -70,6 +70,8 @@ def test_paged_refusals(lib):
     both(OK, page=1 << 30, n_pages=1)
     both(UNSUPPORTED, page=1 << 20, n_pages=1 << 11, ld_pages=1 << 11)
     both(UNSUPPORTED, B=(1 << 16) + 1)
+    heads = dict(H=1 << 8, ld_t=1 << 15)
+    both(UNSUPPORTED, B=1 << 16, q=_rows(**heads), out=_rows(data=2 * F, **heads), k=_cache(H=1 << 8), v=_cache(H=1 << 8))
     both(UNSUPPORTED, q=_rows(T=1 << 23), out=_rows(T=1 << 23))
     both(PARAM, window=-1), both(PARAM, first=-1), both(PARAM, scale=float("nan")), both(PARAM, scale=float("inf"))
     both(PARAM, scale=3e38)
@@ -114,7 +116,7 @@ def test_norm_refusals(lib):
     for eps in (-1e-6, float("nan"), float("inf")):
         assert call(eps=eps) == PARAM
     assert call(weight=F + 8) == ALIGN and call(x=_rows(data=F + 8)) == ALIGN and call(out=_rows(ld_t=1028)) == ALIGN
-    many = dict(T=1 << 22, H=8)
+    many = dict(T=1 << 25, H=8)
     assert call(x=_rows(**many), out=_rows(data=2 * F, **many)) == UNSUPPORTED
     # the residual and its sum
     r, t = _rows(data=3 * F, dtype=F32), _rows(data=4 * F, dtype=F32)

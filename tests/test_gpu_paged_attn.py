@@ -452,8 +452,149 @@ def test_refusals():
                dict(ws=small.float())):
         with pytest.raises(ValueError):
             idx.idx_paged_attn(**(good | kw))
-    for kw, status in ((dict(page=3), 6), (dict(window=-1), 3), (dict(first=-1), 3), (dict(q=q[:, :3]), 2),
+    for kw in (dict(window=-1), dict(first=-1), dict(page=-16), dict(window=2 ** 32 + 5)):
+        with pytest.raises(ValueError):
+            idx.idx_paged_attn(**(good | kw))
+    for kw, status in ((dict(page=3), 6), (dict(page=0), 6), (dict(q=q[:, :3]), 2),
                        (dict(v=caches(92, 64, 2, 64, F16, False)[0]), 4), (dict(scale=float("nan")), 3)):
         with pytest.raises(idx.IdxError) as e:
             idx.idx_paged_attn(**(good | kw))
         assert e.value.status == status
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("where", ["codes", "scale"])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("T", [2, 150])
+def test_quantised_values_that_are_not_finite(where, which, T, fp8):
+    """The same of E4M3 codes and scales (of a value in 16 bits where there are none), for few rows and for many."""
+    if where == "scale" and not fp8:
+        pytest.skip("no scales")
+    n = 200
+    cu, lens, pages, slots = batch(100, [T], [n], 16)
+    k, v = caches(101, slots, 2, 64, F16, fp8)
+    q = queries(102, T, 8, 64, F16)
+    run = lambda: idx.idx_paged_attn(q.cuda(), k, v, gpu(pages), gpu(cu), gpu(lens), 0.1, page=16)
+    clean = run()
+    key = n - T + T // 2                          # of row T // 2
+    slot = int(pages[0, key // 16]) * 16 + key % 16
+    c = k if which == "k" else v
+    if where == "scale":
+        c.scale[slot, 1] = float("inf")
+    elif fp8:
+        c.data[slot, 1, 7] = 0xFF
+    else:
+        c.data[slot, 1, 7] = float("nan")
+    dirty = run()
+    sees = torch.zeros((T, 8), dtype=torch.bool)
+    sees[T // 2:, 4:] = True
+    assert torch.equal(clean[0].cpu()[~sees], dirty[0].cpu()[~sees])
+    assert torch.equal(clean[1].cpu()[~sees], dirty[1].cpu()[~sees])
+    got = dirty[0].cpu()[sees].float()
+    if which == "v":
+        wrong = ~torch.isfinite(got)
+        if where == "scale":
+            # every dim whose code is not zero, and NaN where it is
+            assert wrong.all()
+        else:
+            assert wrong[:, 7].all() and wrong.sum() == wrong[:, 7].sum()
+        assert torch.equal(clean[1].cpu(), dirty[1].cpu())
+    elif where == "codes":
+        assert torch.isnan(got).all()
+
+
+def test_more_requests_than_are_divided():
+    """5000 single rows and small chunks; rows of no request between none."""
+    rng = np.random.default_rng(103)
+    new = rng.integers(0, 4, 5000)
+    lens = new + rng.integers(0, 40, 5000)
+    b = batch(104, new, lens, 8)
+    k, v = caches(105, b[3], 1, 64, BF16, False)
+    T = int(new.sum())
+    check(queries(106, T, 4, 64, BF16), k, v, b, 8, 0.125, rows=sorted(rng.choice(T, 300, replace=False)))
+
+
+@pytest.mark.parametrize("new", [[3, 1], [20, 2]])
+def test_more_heads_than_a_tile_has_rows(new):
+    b = batch(107, new, [100, 333], 16)
+    k, v = caches(108, b[3], 1, 64, BF16, False)
+    check(queries(109, sum(new), 300, 64, BF16), k, v, b, 16, 0.125)
+
+
+@pytest.mark.parametrize("new", [[1], [70]])
+def test_slots_past_32_bits_apart(new):
+    """16 slots of a page spread over more than 2^32 bytes."""
+    ld = (1 << 28) + 1024                         # bytes, E4M3
+    n, rows = 30, 32
+    flat = torch.empty(rows * ld, dtype=torch.uint8, device="cuda")
+    small, wide = [], []
+    for i in range(2):
+        c = idx.Cache.empty(rows, 2, 64)
+        x = (torch.randn((rows, 2, 64), generator=torch.Generator().manual_seed(110 + i))).to(BF16)
+        idx.idx_cache_write([idx.Write(x.cuda(), c)])
+        d = flat.as_strided((rows, 2, 64), (ld, 64, 1), 512 * i)
+        d.copy_(c.data)
+        small.append(c)
+        wide.append(idx.Cache(d, c.scale))
+    q = queries(112, sum(new), 8, 64, BF16).cuda()
+    args = (gpu([[1, 0]]), gpu([0, new[0]]), gpu([n]), 0.1)
+    a, b = (idx.idx_paged_attn(q, *c, *args, page=16) for c in (small, wide))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_layer_of_a_chunk_and_a_step():
+    """Norm with the residual, projections, rotation into the caches, attention over everything and over a window, the
+    next norm: a chunk of two requests, then a token of each, against the same in 64 bits."""
+    torch.manual_seed(0)
+    N, Hq, Hkv, D, page = 512, 8, 2, 64, 16
+    g = torch.Generator().manual_seed(113)
+    w = {n: (torch.randn(s, generator=g) * s[0] ** -0.5).cuda() for n, s in
+         (("q", (N, Hq * D)), ("k", (N, Hkv * D)), ("v", (N, Hkv * D)), ("o", (Hq * D, N)))}
+    gain = (1 + 0.1 * torch.randn(N, generator=g)).cuda()
+    plan = idx.Rotary.make(D)
+    k, v = (idx.Cache.empty(16 * 8, Hkv, D, idx.IDX_K_BF16) for _ in range(2))
+    pages = gpu([[5, 2, 7], [0, 3, 6]])
+    held, x_all = [0, 0], [[], []]
+    freq = plan.freq.cpu().numpy()
+
+    def turn(x, pos):                            # [n, H, D] fp64
+        a = np.asarray(pos)[:, None, None] * freq
+        lo, hi = x[..., :D // 2], x[..., D // 2:]
+        return np.concatenate([lo * np.cos(a) - hi * np.sin(a), hi * np.cos(a) + lo * np.sin(a)], -1)
+
+    for new in ([30, 9], [1, 1], [1, 1]):
+        T = sum(new)
+        x = torch.randn((T, N), generator=g).to(BF16).cuda()
+        residual = torch.randn((T, N), generator=g).to(BF16).cuda()
+        total = torch.empty_like(residual)
+        to = idx.Cache.empty(T, N // 128, 128)
+        y = idx.idx_rms_norm(x, gain, residual=residual, total=total, to=to)
+        h = x.double() + residual.double()
+        want = (h / (h.square().mean(-1, keepdim=True) + 1e-6).sqrt() * gain.double())
+        assert ((y.double() - want).abs() <= 2.0 ** -8 * 1.01 * want.abs() + 1e-30).all()
+        back = idx.idx_cache_read(to, dtype=torch.float32).view(T, N).double()
+        amax = want.view(T, -1, 128).abs().amax(-1, keepdim=True).expand(-1, -1, 128).reshape(T, N)
+        assert ((back - want).abs() <= 2.0 ** -4 * 1.01 * want.abs() + 2.0 ** -10 / 448 * 1.01 * amax).all()
+        pos = np.concatenate([np.arange(held[b], held[b] + n) for b, n in enumerate(new)])
+        slot = np.concatenate([pages[b].cpu().numpy()[np.arange(held[b], held[b] + n) // page] * page
+                               + np.arange(held[b], held[b] + n) % page for b, n in enumerate(new)])
+        proj = {n: (y.float() @ w[n]).to(BF16).view(T, -1, D) for n in "qkv"}
+        idx.idx_cache_write([idx.Write(proj["k"], k, slot=gpu(slot), rotary=plan, pos=gpu(pos)),
+                             idx.Write(proj["v"], v, slot=gpu(slot))])
+        q = idx.idx_rope(proj["q"], gpu(pos), plan)
+        held = [a + n for a, n in zip(held, new)]
+        cu = np.cumsum([0] + new)
+        for window, first in ((0, 0), (12, 2)):
+            out, lse = idx.idx_paged_attn(q, k, v, pages, gpu(cu), gpu(held), D ** -0.5, page=page, window=window, first=first)
+            compare(out, lse, q.cpu(), k, v, pages.cpu().numpy(), page, cu, held, D ** -0.5, window, first)
+        for b in range(2):
+            x_all[b].append(proj["k"][cu[b]:cu[b + 1]].double().cpu().numpy())
+        x2 = (out.reshape(T, Hq * D).float() @ w["o"]).to(BF16)
+        y2 = idx.idx_rms_norm(x2, gain, residual=total)        # in place: the stream of the layers
+        assert torch.isfinite(y2).all()
+    # what the cache holds is each key turned to its place
+    for b in range(2):
+        keys = np.concatenate(x_all[b])
+        at = pages[b].cpu().numpy()[np.arange(held[b]) // page] * page + np.arange(held[b]) % page
+        want = turn(keys, np.arange(held[b]))
+        assert (np.abs(k.data.cpu().double().numpy()[at] - want) <= 2.0 ** -8 * 1.01 * np.abs(want) + 2.0 ** -20).all()
