@@ -127,18 +127,23 @@ __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
 PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len) {
   PagedPlan p{};
   const int32_t live = B < T ? (B > 0 ? B : 1) : (T > 0 ? T : 1);   // requests that can have rows
-  const int64_t need = (int64_t)((T + live - 1) / live) * G;        // rows of a request and cache head, about
-  p.chunk = need > 32;
+  // Rows of a request and cache head, about: tokens times query heads.  Up to 64 of them, and single tokens of up to 128
+  // heads, take 16 or 32 rows to a workgroup and read the keys twice or four times, the later times out of a cache; the chunk
+  // kernel, which reads them once, keeps one wave of four busy then.  us, 16 or 32 rows and chunks, 128 dims, bf16 and E4M3:
+  // a token of 64 heads on 6603 keys 16, 42 and 16, 48; 64 such on 16384 133, 153 and 101, 180; 16 of 128 heads on 4096 35,
+  // 40 and 35, 43; 16 times 8 tokens of 8 heads on 8192 138, 143 and 110, 172.
+  const int64_t need = (int64_t)((T + live - 1) / live) * G;
+  p.chunk = need > 64 && !(T == live && G <= 128);
   p.M = p.chunk ? 256 : need > 16 ? 32 : 16;
   p.Gt = G < p.M ? G : p.M;
   p.blocks = (G + p.Gt - 1) / p.Gt;
   p.R = p.M / p.Gt;
   const int64_t mu = (int64_t)Hkv * p.blocks;
-  const int32_t kt = p.chunk ? 64 : 32;
   p.slots = p.chunk ? (D == 64 ? 512 : 256) : 512;
-  p.min_tiles = p.chunk ? 8 : 4;
+  p.min_tiles = 4;
   const int64_t divided = (T / p.R + live) * mu;      // row tiles at most
-  p.divide = divided < (p.chunk ? 3 : 6) * p.slots && max_len > 2 * p.min_tiles * kt && B <= 4096;
+  // (More requests than 4096 would take each workgroup longer to look through than the division could save.)
+  p.divide = divided < (p.chunk ? 3 : 6) * p.slots && max_len > (p.chunk ? 512 : 256) && B <= 4096;
   if (p.divide) {
     p.tiles = divided;
     p.max_items = divided + 2 * p.slots + p.slots / 8 + mu;

@@ -139,12 +139,12 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
     if (!CHUNK && (float)most <= 1.25f * share) chunk = most;
     chunk = max(chunk, 1);
     if constexpr (CHUNK) {
-      // Few and long items: the longest list in 1 to 8 parts, whichever would be through first.  Equal items run in rounds of
-      // `slots`; unequal ones end within one item of an even share.  A divided item costs its partial output and the join,
-      // about 8 tiles' time.
+      // Few and long items: the longest list in as many parts, up to 16, as would be through first.  Equal items run in rounds of
+      // `slots`; unequal ones end within one item of an even share.  An item takes about 5 tiles' time besides its tiles, and
+      // a division 4 for the partial outputs and the join.
       int64_t best = (int64_t)1 << 62;
       chunk = max(most, 1);
-      for (int s = 1; s <= 8; ++s) {
+      for (int s = 1; s <= 16; s += s < 4 ? 1 : 2) {
         const int32_t size = max((most + s - 1) / s, 1);
         if (s > 1 && size < a.min_tiles) break;
         int32_t items = 0;
@@ -154,8 +154,9 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
         }
         if (s > 1 && (int64_t)items * mu > a.max_items) break;
         const int64_t rounds = ((int64_t)items * mu + a.slots - 1) / a.slots;
-        const int64_t even = rounds * size, uneven = (int64_t)share + size;
-        const int64_t t = min(even, uneven) + (s > 1 ? 8 * rounds : 0);
+        const int64_t even = rounds * (size + 5);
+        const int64_t uneven = (int64_t)(share + 5.f * (float)items * (float)mu / (float)a.slots) + size;
+        const int64_t t = min(even, uneven) + (s > 1 ? 4 * rounds : 0);
         if (t < best) {
           best = t;
           chunk = size;
