@@ -196,7 +196,8 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
       w.row0 = (n - 1 - tile) * R;
       w.first_item = before + tile;
       w.next = n;
-      return BY == ITEM || (w.first_item >= 0 && ((int64_t)w.first_item + (int64_t)(w.splits - 1) * n + 1) * a.Hkv * a.blocks <= a.max_items);
+      const int64_t last = BY == ITEM ? (int64_t)id : (int64_t)w.first_item + (int64_t)(w.splits - 1) * n;
+      return w.first_item >= 0 && (last + 1) * a.Hkv * a.blocks <= a.max_items;
     }
     items += __builtin_amdgcn_readlane(upto, 63);
     if constexpr (BY == TILE) tiles += __builtin_amdgcn_readlane(tiles_upto, 63);

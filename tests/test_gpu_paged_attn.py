@@ -1,4 +1,6 @@
 """Attention over every key, or a window, of a paged cache against its formula in 64 bits."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -598,3 +600,27 @@ def test_a_layer_of_a_chunk_and_a_step():
         at = pages[b].cpu().numpy()[np.arange(held[b]) // page] * page + np.arange(held[b]) % page
         want = turn(keys, np.arange(held[b]))
         assert (np.abs(k.data.cpu().double().numpy()[at] - want) <= 2.0 ** -8 * 1.01 * np.abs(want) + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [24, 1500])
+def test_bounds_that_go_back_stay_inside_the_workspace(fp8, T):
+    """cu_q that is not ascending counts its rows several times over: results mean nothing, but bytes behind the workspace,
+    and rows of no request, are left alone."""
+    B, Hq, Hkv, page = 40, 24, 3, 16
+    k, v = caches(120, 64 * page, Hkv, 64, BF16, fp8)
+    q = queries(121, T, Hq, 64, BF16).cuda()
+    pages = torch.arange(64, dtype=torch.int32, device="cuda").repeat(B, 1)
+    cu = gpu([(T - 4 if b % 2 else 0) for b in range(B + 1)])
+    lens = gpu([64 * page] * B)
+    need = ctypes.c_size_t()
+    out, lse = torch.full_like(q, 7.0), torch.full((T, Hq), 7.0, device="cuda")
+    a = idx.idx_paged(idx._rows(q, "q"), idx._rows(out, "out"), k._struct, v._struct, pages.data_ptr(), 64, 64, page,
+                      cu.data_ptr(), lens.data_ptr(), B, 0, 0, 0.125, lse.data_ptr())
+    lib = idx.load_library()
+    assert lib.idx_paged_attn_workspace(a, need) == 0 and need.value > 0
+    ws = torch.full((need.value + (64 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    assert lib.idx_paged_attn(a, ws.data_ptr(), need.value, None) == 0
+    torch.cuda.synchronize()
+    assert (ws[need.value:] == 0xA5).all()
+    assert (out[T - 4:] == 7.0).all() and (lse[T - 4:] == 7.0).all()
