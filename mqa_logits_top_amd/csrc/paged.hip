@@ -48,43 +48,66 @@ __global__ __launch_bounds__(JOIN) void join_tile_kernel(PagedArgs a, int M, int
   }
 }
 
-// Joins the parts of one row and head, JOIN / (D / 4) of them at a time: few rows, whose keys may be in many parts.
+// Joins the parts of one row and head, JOIN / (D / 4) of them at a time: few rows, whose keys may be in many parts.  Each
+// group of threads keeps a reference of its own, so that a part's reference, sum and values are requested together: the
+// kernel is three latencies long (the batch, the parts, the store).
 template <bool BF16, int D>
 __global__ __launch_bounds__(JOIN) void join_row_kernel(PagedArgs a, int M) {
-  constexpr int QUADS = D / 4, GROUPS = JOIN / QUADS;
+  constexpr int QUADS = D / 4, GROUPS = JOIN / QUADS, AT_ONCE = 4;
   __shared__ __attribute__((aligned(16))) float acc[GROUPS][D];
-  __shared__ float sums[GROUPS];
+  __shared__ float2 ml[GROUPS];
   const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
   const int t = (int)(blockIdx.x / (uint32_t)a.Hq), hq = (int)(blockIdx.x % (uint32_t)a.Hq);
-  if (!*a.chunk) return;
   Item found;
   if (!find_item<32, false, ROW>(a, (uint32_t)t, found) || found.splits == 1) return;
   const Item w = uniform(found);
   const int kvh = hq / a.G, hb = (hq - kvh * a.G) / a.Gt, h = hq - kvh * a.G - hb * a.Gt;
   const int row = (t - w.r.from - w.row0) * a.Gt + h;
   const int64_t at0 = ((int64_t)w.first_item * mu + hb * a.Hkv + kvh) * M + row, step = (int64_t)w.next * mu * M;
-  const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS, lane = threadIdx.x & 63;
-  float top = NEG_INF;   // every wave for itself
-  for (int s = lane; s < w.splits; s += 64) top = __builtin_fmaxf(top, a.part_ml[2 * (at0 + s * step)]);
-  top = wave_reduce_f32(top, [](float x, float y) { return __builtin_fmaxf(x, y); });
-  const float ref = top == NEG_INF ? 0.f : top;
-  float total = 0.f;
+  const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS;
+  float top = NEG_INF, total = 0.f;
   f32x4 r = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = gr; s < w.splits; s += GROUPS) {
-    const int64_t at = at0 + s * step;
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
-    total += f * a.part_ml[2 * at + 1];
-    r += f * *(const f32x4 *)(a.part + at * D + d);
+  for (int s0 = gr; s0 < w.splits; s0 += AT_ONCE * GROUPS) {
+    float2 m[AT_ONCE];
+    f32x4 x[AT_ONCE];
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const int s = s0 + u * GROUPS;
+      m[u] = make_float2(NEG_INF, 0.f);
+      x[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (s < w.splits) {
+        m[u] = *(const float2 *)(a.part_ml + 2 * (at0 + s * step));
+        x[u] = *(const f32x4 *)(a.part + (at0 + s * step) * D + d);
+      }
+    }
+    float to = top;
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) to = __builtin_fmaxf(to, m[u].x);
+    const float ref = to == NEG_INF ? 0.f : to, by = __builtin_amdgcn_exp2f(top - ref);
+    total *= by;
+    r *= by;
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const float f = __builtin_amdgcn_exp2f(m[u].x - ref);
+      total += f * m[u].y;
+      r += f * x[u];
+    }
+    top = to;
   }
   *(f32x4 *)&acc[gr][d] = r;
-  if (d == 0) sums[gr] = total;
+  if (d == 0) ml[gr] = make_float2(top, total);
   __syncthreads();
   if (gr) return;
 #pragma unroll
-  for (int x = 1; x < GROUPS; ++x) {
-    r += *(const f32x4 *)&acc[x][d];
-    total += sums[x];
+  for (int x = 1; x < GROUPS; ++x) top = __builtin_fmaxf(top, ml[x].x);
+  const float ref = top == NEG_INF ? 0.f : top;
+  total = 0.f;
+  r = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int x = 0; x < GROUPS; ++x) {
+    const float f = __builtin_amdgcn_exp2f(ml[x].x - ref);
+    r += f * *(const f32x4 *)&acc[x][d];
+    total += f * ml[x].y;
   }
   r *= finish(total);
   *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)hq * a.out_h + 2 * d) =

@@ -115,12 +115,15 @@ __device__ __forceinline__ bool find_item(const PagedArgs &a, uint32_t id, Item 
     }
     return x;
   };
+  uint32_t left = 1;       // the division that the launch's first items left, requested beside the lengths
+  if constexpr (BY != ITEM) left = *a.chunk;
   const Mine mine0 = load(0);
+  if (!left) return false; // nothing is divided
   auto at = [&](int b0) { return b0 ? load(b0) : mine0; };
   auto parts = [&](const Mine &x, int32_t size) { return max((x.c + size - 1) / size, 1); };
   int32_t chunk;           // key tiles of an item at most
   if constexpr (BY != ITEM) {
-    chunk = (int32_t)*a.chunk;
+    chunk = (int32_t)left;
   } else {
     // what the launch has to do, in key tiles
     const int32_t mu = a.Hkv * a.blocks;
