@@ -538,6 +538,11 @@ def _new_rows(x: torch.Tensor, dtype: int, T: int, H: int, D: int) -> idx_rows:
     return idx_rows(x.data_ptr(), H * D, D, dtype, T, H, D)
 
 
+def _new_like(x: torch.Tensor) -> torch.Tensor:
+    """Contiguous, with x's sizes and type.  (empty_like keeps x's strides; it takes the host 0.6 us less.)"""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 class _on_stream:
     """The calls below run on the stream given, or on the current stream of the tensors' device: outputs and
     workspaces allocated inside belong to it.  Where that is the current stream already, there is nothing to
@@ -832,7 +837,7 @@ def idx_paged_attn(q: torch.Tensor, k: Cache, v: Cache, pages: torch.Tensor, cu_
     lib = load_library()
     with _on_stream(device, stream) as st:
         if out is None:
-            out = q.new_empty(q.shape)
+            out = _new_like(q)
             to = _new_rows(out, rows.dtype, *q.shape)
         elif out.device != device:
             raise ValueError(f"out on {out.device} for q on {device}")
@@ -917,7 +922,7 @@ def idx_rms_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, eps: fl
                 raise ValueError(f"out: {list(shape)} on {device}, got {list(out.shape)} on {out.device}")
             n.out = _norm_rows(out, "out")
         elif with_out:
-            out = x.new_empty(shape)
+            out = _new_like(x)
             n.out = _new_rows(out, rows.dtype, rows.T, rows.H, rows.D)
         s = load_library().idx_rms_norm(n, st)
     if s:
