@@ -6,7 +6,7 @@
 // operand read from LDS then feeds two matrix instructions; four waves share a tile, so that a key comes from memory once
 // for 256 rows; what the registers then hold (queries, two tiles' scores, outputs) leaves room for one wave a SIMD, two with
 // 64 dims.  2048 rows of 32 heads on 8, 65536 keys, 128 dims, bf16: 2070 us, 1045 TFLOP/s (a large library product: 1190);
-// 1000 of 64 heads on to 30001 keys, E4M3, whose codes every wave converts for itself: 1330 us, 630.  What bounds it is one
+// 1000 of 64 heads on to 30001 keys, E4M3, whose codes every wave converts for itself: 1730 us, 484.  What bounds it is one
 // wave's issue, an instruction in 4 cycles, an exponential in 16: of the 4700 cycles of a tile 57% are issue, 21% waits for
 // results, 21% waits for LDS and the other waves; the matrix pipes are busy for 47%.  Moving the second product of 32 keys
 // behind the first product of the next 64, so that weights lie beside both, gave 1% and cost E4M3 16%: not kept.
@@ -60,8 +60,9 @@ constexpr int chunk_lds() {
 // address.
 template <bool BF16, bool FP8, int D, bool RUNS>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(PagedArgs a) {
-  constexpr bool PV_BF16 = BF16 || FP8;   // weights times E4M3 scales need bf16's range
-  constexpr bool TWO = FP8 && !BF16;      // ... and, for fp16 results, two parts
+  // E4M3: a key's scale enters its weight, which then needs bf16's range, and two parts of it, so that a value is not rounded
+  // by its scale and again as a result.  (1000 rows of 64 heads on to 30001 keys: 1730 us, 1325 with one part.)
+  constexpr bool PV_BF16 = BF16 || FP8;
   constexpr float LIFT = !PV_BF16 ? 7.f : 0.f;
   constexpr int RB = FP8 ? D : 2 * D;     // bytes of a cache row
   constexpr int CH = RB / 16;             // its 16-byte chunks
@@ -463,7 +464,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         y *= vsc[i % 4 + 1];
       }
       uint32_t b = pack2<PV_BF16>(x, y);
-      if constexpr (TWO) {
+      if constexpr (FP8) {
         uint32_t r = pack2<true>(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xFFFF0000u));
         asm volatile("" : "+v"(r));
         rest[m][i / 8][i % 8 / 2] = r;
@@ -477,9 +478,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
       if constexpr (FP8)
         x = u32x4{codes2<true, false>(x.x), codes2<true, true>(x.x), codes2<true, false>(x.y), codes2<true, true>(x.y)};
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        o[m][d] = mfma32<PV_BF16>(x, p[m][u], o[m][d]);
-        if constexpr (TWO) o[m][d] = mfma32<true>(x, rest[m][u], o[m][d]);
+      for (int m = 0; m < 2; ++m) o[m][d] = mfma32<PV_BF16>(x, p[m][u], o[m][d]);
+      if constexpr (FP8) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) o[m][d] = mfma32<true>(x, rest[m][u], o[m][d]);
       }
     };
     meet();
