@@ -476,6 +476,7 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
  * rounded before the second product, as there: by at most 2^-8 of their value with bf16 caches; with fp16 ones by 2^-11, and
  * 2^-32 of the row's largest weight for those below 2^-21 of it; with E4M3 caches, where a weight is the product with its
  * value's scale, by 2^-16 whatever q's type is.
+ * With 16-bit caches the output is divided by the sum of the weights as rounded; lse comes from the unrounded ones.
  * The sums are divided last: values within a factor of 2^8 len_k of fp32's largest number can overflow them.
  * A call's results are bitwise repeatable; a row's bits depend on the sizes and lengths of the call, by which its keys
  * are divided, and not on what other rows hold.

@@ -34,7 +34,7 @@ struct PagedArgs {
   int32_t slots, min_tiles;  // ... by aiming at this many workgroups, and at least this many key tiles for each
   int32_t max_items;         // workgroups of the launch
   float *part;               // divided items: [max_items][M][D] unnormalised out, then
-  float *part_ml;            // [max_items][M][2] reference, sum
+  float *part_ml;            // [max_items][M][4] reference, sum, sum of the weights as rounded, nothing
   uint32_t *chunk;           // the division, for the join (0: nothing is divided)
 };
 

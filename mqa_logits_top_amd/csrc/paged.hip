@@ -29,18 +29,20 @@ __global__ __launch_bounds__(JOIN) void join_tile_kernel(PagedArgs a, int M, int
     if (tok >= a.R || h >= heads || w.row0 + tok >= w.r.n) continue;
     const int64_t at0 = ((int64_t)w.first_item * mu + member) * M + row, step = (int64_t)w.next * mu * M;
     float top = NEG_INF;
-    for (int s = 0; s < w.splits; ++s) top = __builtin_fmaxf(top, a.part_ml[2 * (at0 + s * step)]);
+    for (int s = 0; s < w.splits; ++s) top = __builtin_fmaxf(top, a.part_ml[4 * (at0 + s * step)]);
     const float ref = top == NEG_INF ? 0.f : top;
-    float total = 0.f;
+    float total = 0.f, div = 0.f;
     f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int s = 0; s < w.splits; ++s) {
       const int64_t at = at0 + s * step;
-      const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * at] - ref);
-      total += f * a.part_ml[2 * at + 1];
+      const f32x4 m = *(const f32x4 *)(a.part_ml + 4 * at);
+      const float f = __builtin_amdgcn_exp2f(m[0] - ref);
+      total += f * m[1];
+      div += f * m[2];
       r += f * *(const f32x4 *)(a.part + at * D + d);
     }
-    r *= finish(total);
+    r *= finish(div);
     const int64_t t = w.r.from + w.row0 + tok, hq = kvh * a.G + hb * a.Gt + h;
     *(uint2 *)(a.out + t * a.out_t + hq * a.out_h + 2 * d) =
         make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
@@ -55,7 +57,7 @@ template <bool BF16, int D>
 __global__ __launch_bounds__(JOIN) void join_row_kernel(PagedArgs a, int M) {
   constexpr int QUADS = D / 4, GROUPS = JOIN / QUADS, AT_ONCE = 4;
   __shared__ __attribute__((aligned(16))) float acc[GROUPS][D];
-  __shared__ float2 ml[GROUPS];
+  __shared__ f32x4 ml[GROUPS];
   const uint32_t mu = (uint32_t)(a.Hkv * a.blocks);
   const int t = (int)(blockIdx.x / (uint32_t)a.Hq), hq = (int)(blockIdx.x % (uint32_t)a.Hq);
   Item found;
@@ -65,51 +67,53 @@ __global__ __launch_bounds__(JOIN) void join_row_kernel(PagedArgs a, int M) {
   const int row = (t - w.r.from - w.row0) * a.Gt + h;
   const int64_t at0 = ((int64_t)w.first_item * mu + hb * a.Hkv + kvh) * M + row, step = (int64_t)w.next * mu * M;
   const int d = 4 * (threadIdx.x % QUADS), gr = threadIdx.x / QUADS;
-  float top = NEG_INF, total = 0.f;
+  float top = NEG_INF, total = 0.f, div = 0.f;
   f32x4 r = {0.f, 0.f, 0.f, 0.f};
   for (int s0 = gr; s0 < w.splits; s0 += AT_ONCE * GROUPS) {
-    float2 m[AT_ONCE];
-    f32x4 x[AT_ONCE];
+    f32x4 m[AT_ONCE], x[AT_ONCE];
 #pragma unroll
     for (int u = 0; u < AT_ONCE; ++u) {
       const int s = s0 + u * GROUPS;
-      m[u] = make_float2(NEG_INF, 0.f);
+      m[u] = f32x4{NEG_INF, 0.f, 0.f, 0.f};
       x[u] = f32x4{0.f, 0.f, 0.f, 0.f};
       if (s < w.splits) {
-        m[u] = *(const float2 *)(a.part_ml + 2 * (at0 + s * step));
+        m[u] = *(const f32x4 *)(a.part_ml + 4 * (at0 + s * step));
         x[u] = *(const f32x4 *)(a.part + (at0 + s * step) * D + d);
       }
     }
     float to = top;
 #pragma unroll
-    for (int u = 0; u < AT_ONCE; ++u) to = __builtin_fmaxf(to, m[u].x);
+    for (int u = 0; u < AT_ONCE; ++u) to = __builtin_fmaxf(to, m[u][0]);
     const float ref = to == NEG_INF ? 0.f : to, by = __builtin_amdgcn_exp2f(top - ref);
     total *= by;
+    div *= by;
     r *= by;
 #pragma unroll
     for (int u = 0; u < AT_ONCE; ++u) {
-      const float f = __builtin_amdgcn_exp2f(m[u].x - ref);
-      total += f * m[u].y;
+      const float f = __builtin_amdgcn_exp2f(m[u][0] - ref);
+      total += f * m[u][1];
+      div += f * m[u][2];
       r += f * x[u];
     }
     top = to;
   }
   *(f32x4 *)&acc[gr][d] = r;
-  if (d == 0) ml[gr] = make_float2(top, total);
+  if (d == 0) ml[gr] = f32x4{top, total, div, 0.f};
   __syncthreads();
   if (gr) return;
 #pragma unroll
-  for (int x = 1; x < GROUPS; ++x) top = __builtin_fmaxf(top, ml[x].x);
+  for (int x = 1; x < GROUPS; ++x) top = __builtin_fmaxf(top, ml[x][0]);
   const float ref = top == NEG_INF ? 0.f : top;
-  total = 0.f;
+  total = div = 0.f;
   r = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int x = 0; x < GROUPS; ++x) {
-    const float f = __builtin_amdgcn_exp2f(ml[x].x - ref);
+    const float f = __builtin_amdgcn_exp2f(ml[x][0] - ref);
     r += f * *(const f32x4 *)&acc[x][d];
-    total += f * ml[x].y;
+    total += f * ml[x][1];
+    div += f * ml[x][2];
   }
-  r *= finish(total);
+  r *= finish(div);
   *(uint2 *)(a.out + (int64_t)t * a.out_t + (int64_t)hq * a.out_h + 2 * d) =
       make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
   if (d == 0 && a.lse) a.lse[(int64_t)t * a.Hq + hq] = lse_of(top, total);
@@ -170,7 +174,7 @@ PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, in
   if (p.divide) {
     p.tiles = divided;
     p.max_items = divided + 2 * p.slots + p.slots / 8 + mu;
-    p.bytes = ((size_t)p.max_items * p.M * (D + 2) * 4 + 4 + 255) / 256 * 256;
+    p.bytes = ((size_t)p.max_items * p.M * (D + 4) * 4 + 4 + 255) / 256 * 256;
   } else {
     p.tiles = (T / p.R + (int64_t)B) * mu;            // the numbers that tiles are looked up by
     p.max_items = p.tiles;
@@ -196,7 +200,7 @@ hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, con
   a.max_items = (int32_t)plan.max_items;
   a.part = (float *)ws;
   a.part_ml = a.part + (size_t)plan.max_items * plan.M * D;
-  a.chunk = (uint32_t *)(a.part_ml + (size_t)plan.max_items * plan.M * 2);
+  a.chunk = (uint32_t *)(a.part_ml + (size_t)plan.max_items * plan.M * 4);
   const hipError_t e = plan.chunk ? launch_paged_chunk(a, dtype, fmt, D, s) : launch_paged_step(a, dtype, fmt, D, plan.M, s);
   if (e != hipSuccess || !plan.divide) return e;
   if (D == 64) return dtype == IDX_K_BF16 ? launch_join<true, 64>(a, plan, s) : launch_join<false, 64>(a, plan, s);

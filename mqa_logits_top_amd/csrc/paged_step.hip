@@ -30,6 +30,18 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
+// x plus a pair's two values, rounded once.
+template <bool BF16>
+__device__ __forceinline__ float add_pair(float x, uint32_t pair) {
+  if constexpr (BF16) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, pair), v2{(__bf16)1.f, (__bf16)1.f}, x, false);
+  } else {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2, pair), v2{(_Float16)1.f, (_Float16)1.f}, x, false);
+  }
+}
+
 // Over the four lanes that hold one row (l, l ^ 16, l ^ 32, l ^ 48).
 template <class Op>
 __device__ __forceinline__ float over_row(float x, Op op) {
@@ -48,7 +60,7 @@ constexpr int step_wave_lds() {
 }
 template <bool FP8, int D, int MT>
 constexpr int step_lds() {
-  return WAVES * step_wave_lds<FP8, D, MT>() + WAVES * MT * 16 * 8;
+  return WAVES * step_wave_lds<FP8, D, MT>() + WAVES * MT * 16 * 16;
 }
 
 // RUNS: has_runs.
@@ -211,10 +223,11 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
 
   f32x4 o[MT][DN];
   float ref[MT], sum[MT], high[MT];
+  float rounded[MT];   // 16-bit caches: the sum of the weights as rounded, by which the output is divided (attn.hip); no time
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     ref[m] = high[m] = NEG_INF;
-    sum[m] = 0.f;
+    sum[m] = rounded[m] = 0.f;
 #pragma unroll
     for (int d = 0; d < DN; ++d) o[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
@@ -328,6 +341,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
           const float to = all > high[m] ? __builtin_fmaxf(ref[m], product(all, a.scale2) - LIFT) : ref[m];
           const float f = to == ref[m] ? 1.f : __builtin_amdgcn_exp2f(ref[m] - to);
           sum[m] *= f;
+          rounded[m] *= f;
 #pragma unroll
           for (int d = 0; d < DN; ++d) o[m][d] *= f;
           ref[m] = to;
@@ -355,6 +369,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
             y *= vsc[i / 4][i % 4 + 1];
           }
           p[m][i / 2] = pack2<PV_BF16>(x, y);
+          if constexpr (!FP8) rounded[m] = add_pair<BF16>(rounded[m], p[m][i / 2]);
           if constexpr (FP8)
             rest[m][i / 2] =
                 pack2<true>(x - __uint_as_float(p[m][i / 2] << 16), y - __uint_as_float(p[m][i / 2] & 0xFFFF0000u));
@@ -472,14 +487,15 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
 
   // The waves' outputs, references and sums through LDS; quads of dims exchanged against bank conflicts
   constexpr int QUADS = D / 4;
-  float *const ml = (float *)(lds + WAVES * WAVE_LDS);   // [waves][M][2]
+  float *const ml = (float *)(lds + WAVES * WAVE_LDS);   // [waves][M][4]
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const float l = over_row(sum[m], [](float x, float y) { return x + y; });
+    auto plus = [](float x, float y) { return x + y; };
+    const float l = over_row(sum[m], plus), div = FP8 ? l : over_row(rounded[m], plus);
     const int row = m * 16 + c;
 #pragma unroll
     for (int d = 0; d < DN; ++d) *(f32x4 *)(kbuf + row * D * 4 + ((4 * d + g) ^ (c & 7)) * 16) = o[m][d];
-    if (g == 0) *(float2 *)(ml + (wave * M + row) * 2) = make_float2(ref[m], l);
+    if (g == 0) *(f32x4 *)(ml + (wave * M + row) * 4) = f32x4{ref[m], l, div, 0.f};
   }
   __syncthreads();
   for (int x = threadIdx.x; x < M * QUADS; x += 64 * WAVES) {
@@ -487,23 +503,25 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
     if (tok >= a.R || h >= heads || w.row0 + tok >= w.r.n) continue;
     float top = NEG_INF;
 #pragma unroll
-    for (int i = 0; i < WAVES; ++i) top = __builtin_fmaxf(top, ml[(i * M + row) * 2]);
+    for (int i = 0; i < WAVES; ++i) top = __builtin_fmaxf(top, ml[(i * M + row) * 4]);
     const float base = top == NEG_INF ? 0.f : top;
-    float total = 0.f;
+    float total = 0.f, div = 0.f;
     f32x4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) {
-      const float f = __builtin_amdgcn_exp2f(ml[(i * M + row) * 2] - base);
-      total += f * ml[(i * M + row) * 2 + 1];
+      const f32x4 x = *(const f32x4 *)(ml + (i * M + row) * 4);
+      const float f = __builtin_amdgcn_exp2f(x[0] - base);
+      total += f * x[1];
+      div += f * x[2];
       r += f * *(const f32x4 *)(lds + i * WAVE_LDS + row * D * 4 + (y ^ (row & 7)) * 16);
     }
     const int64_t t = w.r.from + w.row0 + tok, hq = head0 + h;
     if (w.splits > 1) {
       const int64_t at = ((int64_t)id * mu + member) * M + row;
       *(f32x4 *)(a.part + at * D + 4 * y) = r;
-      if (y == 0) *(float2 *)(a.part_ml + 2 * at) = make_float2(top, total);
+      if (y == 0) *(f32x4 *)(a.part_ml + 4 * at) = f32x4{top, total, div, 0.f};
     } else {
-      r *= finish(total);
+      r *= finish(div);
       *(uint2 *)(a.out + t * a.out_t + hq * a.out_h + 8 * y) =
           make_uint2(pack2<BF16>(r[0], r[1]), pack2<BF16>(r[2], r[3]));
       if (y == 0 && a.lse) a.lse[t * a.Hq + hq] = lse_of(top, total);

@@ -47,3 +47,28 @@ def test_a_row_that_sees_one_quantised_key_gives_its_value(dtype, D, page, singl
     err = np.abs(out.cpu().double().numpy() - want)
     bound = half_step(want, dtype) + (2.0 ** -16 + 2.0 ** -21) * np.abs(want)
     assert (err <= bound).all(), f"{(err > bound).sum()} off, worst {np.max(err / bound):.2f} of the bound"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page", [1, 16])
+@pytest.mark.parametrize("new,n", [([1], 20), ([1], 9000), ([3, 3], 700), ([140], 700), ([130, 9], 12000), ([300] * 6, 420)])
+def test_values_that_are_all_alike_come_out_as_they_are(dtype, D, page, new, n):
+    """Nearly every weight is rounded the same way, by almost half a step, so that a sum of the weights before they are rounded
+    would be off by that: an average of ones is one to a sum's 2^-24 a term, far below half a step of a result."""
+    H, B = 2, len(new)
+    k, v = (idx.Cache.empty((n + page - 1) // page * page, H, D, {BF16: idx.IDX_K_BF16, F16: idx.IDX_K_F16}[dtype])
+            for _ in range(2))
+    k.data[::16, :, 0] = 1                       # score 1, the others 0
+    v.data[:] = 1
+    q = torch.zeros((sum(new), 8, D), dtype=dtype, device="cuda")
+    q[..., 0] = 1
+    part = 1 + 0.96 * 2.0 ** -BITS[dtype]        # of the others' weights: rounded down to 1, by 0.96 of half a step
+    scale = np.log(2) - np.log(part)             # their weights are exp(-scale) = part / 2
+    pages = gpu(np.arange((n + page - 1) // page)).repeat(B, 1)
+    out, lse = idx.idx_paged_attn(q, k, v, pages, gpu(np.cumsum([0] + new)), gpu([n] * B), scale, page=page)
+    assert (out == 1).all(), out[out != 1]
+    pos = np.concatenate([n - x + np.arange(x) for x in new])
+    high = pos // 16 + 1
+    want = scale + np.log(high + (pos + 1 - high) * part / 2)
+    assert (np.abs(lse.cpu().double().numpy() - want[:, None]) <= 2.0 ** -20 + n * 2.0 ** -24).all()
