@@ -658,17 +658,20 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         bool ok;
         const uint32_t slot = slot_of((uint32_t)table[key >> a.page_sh], key, ok);
         if (!ok) continue;
+        // by the code and the scale, as they were taken out: a product past fp32's range has been counted with its weight
         float scale = 1.f, val[E];
         bool odd[E], some_odd = false;
         if constexpr (FP8) scale = a.v_scale[(int64_t)slot * a.scale_row + kvh];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           const uint8_t *at = vbase + (uint64_t)slot * a.row_bytes + (lane * E + e) * (FP8 ? 1 : 2);
-          if constexpr (FP8)
+          if constexpr (FP8) {
             val[e] = __builtin_amdgcn_cvt_f32_fp8((int)*at, 0) * scale;
-          else
+            odd[e] = (*at & 0x7Fu) == 0x7Fu || !finite(scale);
+          } else {
             val[e] = BF16 ? __uint_as_float((uint32_t) * (const uint16_t *)at << 16) : (float)*(const _Float16 *)at;
-          odd[e] = !finite(val[e]);
+            odd[e] = !finite(val[e]);
+          }
           some_odd |= odd[e];
         }
         if (!__any(some_odd)) continue;
