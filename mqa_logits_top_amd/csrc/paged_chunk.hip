@@ -260,10 +260,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   };
   int vst = 0;        // stage of V(j)
   // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN.  Before such a tile
-  // is used each wave takes them out of its rows of it in LDS; at the end the rows that see them get them.
-  bool odd_seen = false;
+  // (an edge) is used each wave takes them out of its rows of it in LDS; at the end the rows that see them get them.  Those
+  // that no row sees (behind the last key, before the window, without a slot) may be any memory's, and cost no more.
+  int32_t odd_lo = INT32_MAX, odd_hi = -1;   // tiles, from the first to the last, with some that a row sees
   const int32_t p0 = w.r.len - w.r.n + w.row0, p1 = last_key;   // the workgroup's first and last row
+  const int32_t lb0 = a.window ? (int32_t)max((int64_t)p0 - a.window, (int64_t)-1) : -1;
   const int32_t lb1 = a.window ? (int32_t)max((int64_t)p1 - a.window, (int64_t)-1) : -1;
+  auto edge = [&](int32_t k0, uint64_t good) INLINE {
+    return !(k0 + KT - 1 <= p0 && (k0 > lb1 || k0 + KT - 1 < a.first) && good == ~0ull);
+  };
+  auto some_row_sees = [&](int32_t key, bool ok) INLINE { return ok && key <= p1 && (key > lb0 || key < a.first); };
   auto good_keys = [&](int v) INLINE -> uint64_t {   // keys of a tile that have a slot
     const uint32_t id = ids[(v & (IDS - 1)) * KT + lane];
     if constexpr (RUNS) return __ballot(id <= max_page);
@@ -272,7 +278,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
     return __ballot(ok);
   };
   auto clean = [&](int v, int32_t k0, uint64_t good) INLINE {
-    if (k0 + KT - 1 <= p0 && (k0 > lb1 || k0 + KT - 1 < a.first) && good == ~0ull) return;
+    if (!edge(k0, good)) return;
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NSTEP) : "memory");   // its own rows are there
     bool odd = false;
 #pragma unroll
@@ -292,17 +298,24 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         z[x] &= ~bits;
         here |= bits != 0u;
       }
-      if (here) *at = z;
-      odd |= here;
+      if (here) {
+        *at = z;
+        const int r = 16 * wave + i * RPC + my_row;
+        odd |= some_row_sees(k0 + r, (good >> r) & 1u);
+      }
     }
     if constexpr (FP8) {
       float *const at = (float *)(lds + SCALES_AT + ((v & (KSTAGES - 1)) * WAVES + wave) * 256) + 16 + (lane & 15);
       if (!finite(*at)) {
         *at = 0.f;
-        odd = true;
+        const int r = 16 * wave + (lane & 15);
+        odd |= some_row_sees(k0 + r, (good >> r) & 1u);
       }
     }
-    odd_seen |= __any(odd) != 0;
+    if (__any(odd)) {
+      odd_lo = min(odd_lo, v);
+      odd_hi = v;
+    }
     lds_done();
   };
   uint64_t good = 0;
@@ -603,13 +616,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
   // whether any wave left some values out; and the others have read their last tile
   constexpr int OUT_CH = D / 8;   // 16-byte chunks of a row of out
   uint8_t *const mine = lds + wave * 64 * 2 * D;
-  uint32_t *const word = (uint32_t *)(lds + M * 2 * D);
-  static_assert(M * 2 * D + 4 * WAVES <= chunk_lds<FP8, D>(), "the output fits");
+  int32_t *const word = (int32_t *)(lds + M * 2 * D);
+  static_assert(M * 2 * D + 8 * WAVES <= chunk_lds<FP8, D>(), "the output fits");
   if (nv > 0) {
     __syncthreads();
-    if (lane == 0) word[wave] = odd_seen;
+    if (lane == 0) {
+      word[2 * wave] = odd_lo;
+      word[2 * wave + 1] = odd_hi;
+    }
     __syncthreads();
-    odd_seen = (word[0] | word[1] | word[2] | word[3]) != 0u;
+    for (int x = 0; x < WAVES; ++x) {
+      odd_lo = min(odd_lo, uniform(word[2 * x]));
+      odd_hi = max(odd_hi, uniform(word[2 * x + 1]));
+    }
   }
   // lane l holds row l % 32 and dims 32 d + 8 (z / 4) + 4 (l / 32) + z % 4
 #pragma unroll
@@ -647,17 +666,20 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
             *(const u32x4 *)(mine + x * 2 * D + ((ch ^ (x & (OUT_CH - 1))) << 4));
     }
   }
-  if (odd_seen) {
+  if (odd_hi >= 0) {
     asm volatile("");   // stays a branch
     __threadfence();    // the outputs are other lanes'
     constexpr int E = D / 64;
-    for (int j = 0; j < nv; ++j)
+    for (int j = odd_lo; j <= odd_hi; ++j) {
+      const int32_t k0 = key0(j), mine = min(k0 + lane, last_key);
+      bool ok;
+      const uint32_t slot0 = slot_of((uint32_t)table[mine >> a.page_sh], mine, ok);
+      const uint64_t have = __ballot(ok);
+      if (!edge(k0, have)) continue;   // none was taken out
       for (int i = 0; i < KT; ++i) {
-        const int32_t key = key0(j) + i;
-        if (key > last_key) break;
-        bool ok;
-        const uint32_t slot = slot_of((uint32_t)table[key >> a.page_sh], key, ok);
-        if (!ok) continue;
+        const int32_t key = k0 + i;
+        if (!some_row_sees(key, (have >> i) & 1u)) continue;
+        const uint32_t slot = (uint32_t)__builtin_amdgcn_readlane((int)slot0, i);
         // by the code and the scale, as they were taken out: a product past fp32's range has been counted with its weight
         float scale = 1.f, val[E];
         bool odd[E], some_odd = false;
@@ -678,8 +700,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
         for (int row = wave * 64; row < wave * 64 + 64; ++row) {
           const int tok = row / a.Gt, h = row - tok * a.Gt;
           if (tok >= a.R || h >= heads || w.row0 + tok >= w.r.n) continue;
-          const int32_t p1 = w.r.len - w.r.n + w.row0 + tok;
-          if (key > p1 || (a.window && (int64_t)key <= (int64_t)p1 - a.window && key >= a.first)) continue;
+          const int32_t p = w.r.len - w.r.n + w.row0 + tok;
+          if (key > p || (a.window && (int64_t)key <= (int64_t)p - a.window && key >= a.first)) continue;
           const int64_t tq = w.r.from + w.row0 + tok;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -697,6 +719,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(Page
           }
         }
       }
+    }
   }
 }
 

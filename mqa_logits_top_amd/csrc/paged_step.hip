@@ -118,6 +118,8 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
       max_lb = max(max_lb, lb[m]);
     }
   }
+  const int32_t p0 = w.r.len - w.r.n + w.row0;   // keys above lb0, or below a.first, are in the first row's window
+  const int32_t lb0 = a.window ? (int32_t)max((int64_t)p0 - a.window, (int64_t)-1) : -1;
   min_pos = uniform((int32_t)(wave_min((uint32_t)min_pos ^ 0x80000000u) ^ 0x80000000u));
   max_lb = uniform((int32_t)(wave_max((uint32_t)(max_lb + 1)) - 1u));
   const uint32_t whole0 = min_pos - 31 > max_lb ? (uint32_t)max_lb + 1u : ~0u;
@@ -399,9 +401,23 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
       }
       lds_done();
       if (masked) {
-        // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN: they are left
-        // out of the product, and added for the rows that see their keys.
+        // Keys that not every row sees may hold values that are not finite, and weight 0 times those is NaN.  Those of keys
+        // that no row sees (behind the last key, before the window, without a slot: any memory's) become zeros; others are
+        // left out of the product, and added for the rows that see their keys.
+        auto below = [&](int32_t key) INLINE -> uint32_t {   // of the 32 keys from k0 on
+          return key <= k0 ? 0u : key - k0 >= 32 ? ~0u : (1u << (key - k0)) - 1u;
+        };
+        const uint32_t seen = below(last_key + 1) & (~below(lb0 + 1) | below(a.first)) & good_now;
         bool odd = false;
+#pragma unroll
+        for (int i = 0; i < (FP8 ? 2 : 4); ++i) {
+          const uint32_t bits = seen >> (4 * g) >> (FP8 ? 16 * i : 16 * (i >> 1) + 2 * (i & 1));
+          uint32_t keep = 0;
+#pragma unroll
+          for (int y = 0; y < (FP8 ? 4 : 2); ++y) keep |= -((bits >> y) & 1u) & (FP8 ? 0xFFu << (8 * y) : 0xFFFFu << (16 * y));
+#pragma unroll
+          for (int d = 0; d < DN; ++d) vt[d][i] &= keep;
+        }
 #pragma unroll
         for (int d = 0; d < DN; ++d)
 #pragma unroll
@@ -409,7 +425,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
 #pragma unroll
             for (int y = 0; y < 32; y += FP8 ? 8 : 16) odd |= odd_value(vt[d][i] >> y);
         const float *vs1 = (const float *)(kbuf + SCALES_AT + (j & 1) * 256) + 32;
-        if constexpr (FP8) odd |= !finite(vs1[lane & 31]);
+        if constexpr (FP8) odd |= !finite(vs1[lane & 31]) && ((seen >> (lane & 31)) & 1u);
         if (__any(odd)) {
           asm volatile("");
 #pragma unroll
@@ -420,6 +436,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
               for (int y = 0; y < 32; y += FP8 ? 8 : 16)
                 if (odd_value(vt[d][i] >> y)) vt[d][i] &= ~((FP8 ? 0xFFu : 0xFFFFu) << y);
           for (int key = 0; key < KT; ++key) {
+            if (!((seen >> key) & 1u)) continue;
             float scale = 1.f;
             if constexpr (FP8) scale = vs1[key];
             const bool bad_scale = !finite(scale);
