@@ -42,7 +42,7 @@ __device__ __forceinline__ KeyTiles key_tiles(const PagedArgs &a, const Request 
   const int32_t lo = low > 0 ? (int32_t)(low / KT) : 0;   // tile of the first row's window
   k.firsts = (int32_t)(((int64_t)min((int64_t)a.first, (int64_t)lo * KT) + KT - 1) / KT);
   k.base = lo * KT;
-  k.count = k.firsts + (k.hi + KT - 1) / KT - lo;
+  k.count = k.firsts + (k.hi - 1) / KT + 1 - lo;   // (hi may be up to 2^31 - 1)
   return k;
 }
 
