@@ -169,7 +169,8 @@ idx_status check_attn(const idx_attn *a) {
 }
 
 idx::PagedPlan plan_of(const idx_paged *a) {
-  return idx::plan_paged(a->q.T, a->B, a->k.H, a->q.H / a->k.H, a->q.D, a->n_pages * a->page);
+  return idx::plan_paged(a->q.T, a->B, a->k.H, a->q.H / a->k.H, a->q.D, a->n_pages * a->page,
+                         a->k.fmt == IDX_K_FP8_E4M3);
 }
 
 idx_status check_paged(const idx_paged *a) {
@@ -185,7 +186,8 @@ idx_status check_paged(const idx_paged *a) {
   if (a->q.T > 0 && a->B > 0 && (!a->cu_q || !a->len_k || (a->n_pages > 0 && !a->pages))) return IDX_E_NULL;
   if (!aligned(a->pages, 4) || !aligned(a->cu_q, 4) || !aligned(a->len_k, 4)) return IDX_E_ALIGN;
   // workgroups of 256 lanes, fewer than 2^32 lanes
-  return plan_of(a).max_items < (int64_t)1 << 23 ? IDX_OK : IDX_E_UNSUPPORTED;
+  const idx::PagedPlan plan = plan_of(a);
+  return plan.max_items < (int64_t)1 << 23 && plan.grid < (int64_t)1 << 24 ? IDX_OK : IDX_E_UNSUPPORTED;
 }
 
 // Whether two row arrays that start together lie alike; true where they do not.

@@ -32,7 +32,8 @@ struct PagedArgs {
   int32_t Gt, blocks;        // query heads of a row tile, and head blocks of a cache head
   int32_t divide;            // whether keys may be divided over workgroups
   int32_t slots, min_tiles;  // ... by aiming at this many workgroups, and at least this many key tiles for each
-  int32_t max_items;         // workgroups of the launch
+  int32_t max_items;         // workgroups that may have work
+  int32_t grid;              // ... of the launch
   float *part;               // divided items: [max_items][M][D] unnormalised out, then
   float *part_ml;            // [max_items][M][4] reference, sum, sum of the weights as rounded, nothing
   uint32_t *chunk;           // the division, for the join (0: nothing is divided)
@@ -50,9 +51,11 @@ struct PagedPlan {
   int32_t divide, slots, min_tiles;
   int64_t tiles;             // row tiles of the batch at most, times cache heads and head blocks
   int64_t max_items;
+  bool by_xcd;               // all cache heads of an item on one XCD
+  int64_t grid;              // workgroups: max_items, with by_xcd for a multiple of 8 items
   size_t bytes;              // workspace
 };
-PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len);
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len, bool fp8);
 hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, const PagedPlan &plan, void *ws,
                         hipStream_t s);
 hipError_t launch_paged_chunk(const PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, hipStream_t s);

@@ -151,7 +151,7 @@ __global__ void check_paged_kernel(PagedArgs a, uint32_t *word) {
 
 }  // namespace
 
-PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len) {
+PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, int32_t max_len, bool fp8) {
   PagedPlan p{};
   const int32_t live = B < T ? (B > 0 ? B : 1) : (T > 0 ? T : 1);   // requests that can have rows
   // Rows of a request and cache head, about: tokens times query heads.  Up to 64 of them, and single tokens of up to 128
@@ -179,6 +179,8 @@ PagedPlan plan_paged(int32_t T, int32_t B, int32_t Hkv, int32_t G, int32_t D, in
     p.tiles = (T / p.R + (int64_t)B) * mu;            // the numbers that tiles are looked up by
     p.max_items = p.tiles;
   }
+  p.by_xcd = !p.chunk && (fp8 || p.blocks > 1);
+  p.grid = p.by_xcd ? (p.max_items / mu + 8) / 8 * 8 * mu : p.max_items;
   return p;
 }
 
@@ -198,6 +200,7 @@ hipError_t launch_paged(PagedArgs &a, int32_t dtype, int32_t fmt, int32_t D, con
   a.slots = plan.slots;
   a.min_tiles = plan.min_tiles;
   a.max_items = (int32_t)plan.max_items;
+  a.grid = (int32_t)plan.grid;
   a.part = (float *)ws;
   a.part_ml = a.part + (size_t)plan.max_items * plan.M * D;
   a.chunk = (uint32_t *)(a.part_ml + (size_t)plan.max_items * plan.M * 4);

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
   // Workgroup b runs on XCD b % 8.  E4M3 rows of several cache heads share lines, their scales if nothing else: there all
   // heads of an item run on one XCD.
   uint32_t id = blockIdx.x / mu, member = blockIdx.x % mu;
-  if (FP8 || a.blocks > 1) {
+  if (FP8 || a.blocks > 1) {   // PagedPlan::by_xcd
     const uint32_t local = blockIdx.x >> 3;
     id = local / mu * 8 + (blockIdx.x & 7u);
     member = local % mu;
@@ -548,13 +548,11 @@ __global__ __launch_bounds__(64 * WAVES, FP8 && MT == 1 ? 3 : 2) void step_kerne
 
 template <bool BF16, bool FP8, int D, int MT>
 hipError_t launch_tiles(const PagedArgs &a, hipStream_t s) {
-  const int64_t mu = (int64_t)a.Hkv * a.blocks;
-  const int64_t grid = FP8 || a.blocks > 1 ? (a.max_items / mu + 8) / 8 * 8 * mu : a.max_items;
   constexpr int lds = step_lds<FP8, D, MT>();
   if (has_runs(a))
-    hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, true>), dim3((unsigned)grid), dim3(64 * WAVES), lds, s, a);
+    hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, true>), dim3((unsigned)a.grid), dim3(64 * WAVES), lds, s, a);
   else
-    hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, false>), dim3((unsigned)grid), dim3(64 * WAVES), lds, s, a);
+    hipLaunchKernelGGL((step_kernel<BF16, FP8, D, MT, false>), dim3((unsigned)a.grid), dim3(64 * WAVES), lds, s, a);
   return hipGetLastError();
 }
 template <bool BF16, bool FP8>
