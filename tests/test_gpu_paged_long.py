@@ -58,3 +58,39 @@ def test_lengths_up_to_the_largest(T, page, fp8):
             s = np.concatenate([np.arange(first), np.arange(p - window + 1, p + 1)])
             seen.append(s // page % P * page + s % page)
         compare(out, lse, q, k, v, seen, 0.125, pick)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B,rows,Hkv,G,D", [(65, 1, 2, 4, 128), (200, 1, 2, 4, 64), (1000, 1, 1, 8, 128), (130, 4, 1, 8, 128),
+                                            (100, 24, 1, 8, 128), (300, 12, 1, 8, 64), (70, 60, 1, 4, 128)])
+def test_many_requests_whose_keys_are_divided(B, rows, Hkv, G, D, fp8):
+    """More requests than lanes, empty ones among them, with long ones early, in the 65th place and last: the division counts
+    them 64 at a time."""
+    rng = np.random.default_rng(310)
+    page = 16
+    new = rng.integers(0, 2 * rows, B) if rows > 1 else np.ones(B, int)
+    long = [2, 64, B - 1]
+    new[long] = np.maximum(new[long], rows)
+    lens = new + rng.integers(0, 200, B)
+    lens[long] = [7001, 5000, 9003]
+    held = -(-lens // page)
+    order = rng.permutation(held.sum()).astype(np.int32)
+    pages = np.full((B, held.max() + 1), -7, np.int32)
+    for b, at in enumerate(np.cumsum(held) - held):
+        pages[b, :held[b]] = order[at:at + held[b]]
+    cu, T = np.cumsum([0, *new]), int(new.sum())
+    k, v = caches(311, int(held.sum()) * page, Hkv, D, fp8)
+    q = torch.randn((T, Hkv * G, D), generator=torch.Generator().manual_seed(312)).to(BF16).cuda()
+    for window, first in ((0, 0), (3000, 5)):
+        out, lse = idx.idx_paged_attn(q, k, v, gpu(pages), gpu(cu), gpu(lens), 0.1, page=page, window=window, first=first)
+        pick = sorted({int(cu[b + 1]) - 1 for b in long} | {int(cu[b]) for b in long} | set(rng.integers(0, T, 30).tolist()))
+        seen = []
+        for t in pick:
+            b = int(np.searchsorted(cu, t, "right")) - 1
+            p = lens[b] - new[b] + t - cu[b]
+            s = np.arange(p + 1)
+            s = s[(s > p - window) | (s < first)] if window else s
+            seen.append(pages[b, s // page] * page + s % page)
+        compare(out, lse, q, k, v, seen, 0.1, pick)
+        again = idx.idx_paged_attn(q, k, v, gpu(pages), gpu(cu), gpu(lens), 0.1, page=page, window=window, first=first)
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
