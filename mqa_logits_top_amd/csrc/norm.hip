@@ -15,6 +15,8 @@
 namespace idx {
 namespace {
 
+constexpr float SMALL_EPS = 0x1p-100f;   // squares lose up to 2^-150 each
+
 // x summed over aligned groups of 2^sh lanes.
 __device__ __forceinline__ float group_sum(float x, int sh) {
   auto add = [&](int on, int moved) { return on ? x + __uint_as_float((uint32_t)moved) : x; };
@@ -114,11 +116,38 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void norm_kernel(Norm
       for (int e = 0; e < 8; ++e) v[i][e] += r[e];
       store8<F32>(j.total.p + t * j.total.t + h * j.total.h + (int64_t)(c + i * stride) * 8 * rs, j.total.dtype, v[i]);
     }
+  }
+  const int wave = threadIdx.x >> 6, wave0 = WAVES > 1 ? wave / WAVES * WAVES : 0;
+  // An eps too small to cover what squares lose below fp32's normal numbers (the whole launch's): rows are multiplied by a
+  // power of two, which no other rounding notices, so that their largest value, or eps's root, comes to 1.
+  float eps = j.eps;
+  if (eps < SMALL_EPS) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[i][e]) & 0x7FFFFFFFu);
+    top = group_max(top, sh);
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & 63) == 0) tops[wave] = top;
+      __syncthreads();
+      top = tops[wave0];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) top = max(top, tops[wave0 + w]);
+    }
+    int up = top >= INF ? 0 : max(-__builtin_amdgcn_frexp_expf(__uint_as_float(top)), 0);
+    if (eps > 0.f) up = min(up, -__builtin_amdgcn_frexp_expf(eps) / 2);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = __builtin_amdgcn_ldexpf(v[i][e], up);
+    eps = __builtin_amdgcn_ldexpf(eps, 2 * up);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(v[i][e], v[i][e], sum);
-  }
   sum = group_sum(sum, sh);
-  const int wave = threadIdx.x >> 6, wave0 = WAVES > 1 ? wave / WAVES * WAVES : 0;
   if constexpr (WAVES > 1) {
     if ((threadIdx.x & 63) == 0) parts[wave] = sum;
     __syncthreads();
@@ -126,7 +155,7 @@ __global__ __launch_bounds__(WAVES > 4 ? 64 * WAVES : 256) void norm_kernel(Norm
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) sum += parts[wave0 + w];
   }
-  const float rstd = 1.f / __builtin_sqrtf(sum / (float)j.D + j.eps);
+  const float rstd = 1.f / __builtin_sqrtf(sum / (float)j.D + eps);
   uint32_t top = 0;
   uint8_t *const out = j.out.p + t * j.out.t + h * j.out.h;
   const int os = F32 && j.out.dtype == IDX_K_F32 ? 4 : 2;
