@@ -466,7 +466,8 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
  * G = Hq / H consecutive query heads to a cache head.  lse (nullable): [T, Hq] fp32, ln of the sum of the exponentials.
  * A row that sees no key (p < 0, as where len_k[b] is short of the request's rows) gets zeros and -inf.  Rows in no
  * request (before cu_q[0], at or behind cu_q[B]) are left as they are, in out and in lse.  One row a request is a decode
- * step; requests of any lengths, zero among them, share a call.
+ * step; requests of any lengths, zero among them, share a call.  (It is set up for the mean of their rows: a long chunk and
+ * dozens of single tokens may take less in two calls, up to 30% where this was measured.)
  * cu_q (not descending, within [0, T]), len_k and pages are read on the device: the call can be captured and replayed with
  * other lengths in them, and is sized by T, B and n_pages * page, which bounds len_k (a longer one is taken as that).
  * A key whose slot is outside the caches does not count.  Slots that no row of a request sees are not read, or read and

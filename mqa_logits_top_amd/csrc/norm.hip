@@ -5,8 +5,8 @@
 // first is used.  Narrow rows share a wave, wide ones take 1 to 16 waves.  The squares' sum goes over the lanes by DPP and,
 // with several waves, through LDS in a fixed order: results are repeatable.
 //
-// Memory bounds it: 16384 rows of 8192, bf16, with residual and E4M3 codes, 162 us, 5.8 TB/s; 2048 rows of 64 heads of 128,
-// 12.8 us, 5.2; one row 3.6 us, of which the launch is 3.
+// Memory bounds it.  Medians of traced launches: 16384 rows of 8192, bf16, with residual and E4M3 codes, 165 us, 5.7 TB/s;
+// 2048 rows of 64 heads of 128, 14.8 us, 4.5; one row 3.9 us, of which the launch is 3.
 #include "norm.h"
 
 #include "common.h"

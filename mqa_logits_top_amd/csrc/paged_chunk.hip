@@ -5,11 +5,12 @@
 // holds one row's scores and the weights are the second product's operands as they come out.  64 rows a wave, because every
 // operand read from LDS then feeds two matrix instructions; four waves share a tile, so that a key comes from memory once
 // for 256 rows; what the registers then hold (queries, two tiles' scores, outputs) leaves room for one wave a SIMD, two with
-// 64 dims.  2048 rows of 32 heads on 8, 65536 keys, 128 dims, bf16: 2070 us, 1045 TFLOP/s (a large library product: 1190);
-// 1000 of 64 heads on to 30001 keys, E4M3, whose codes every wave converts for itself: 1730 us, 484.  What bounds it is one
-// wave's issue, an instruction in 4 cycles, an exponential in 16: of the 4700 cycles of a tile 57% are issue, 21% waits for
-// results, 21% waits for LDS and the other waves; the matrix pipes are busy for 47%.  Moving the second product of 32 keys
-// behind the first product of the next 64, so that weights lie beside both, gave 1% and cost E4M3 16%: not kept.
+// 64 dims.  Among captured calls, joins included: 2048 rows of 32 heads on 8, 65536 keys, 128 dims, bf16: 2096 us, 1033
+// TFLOP/s (a large library product: 1200); 1000 of 64 heads on to 30001 keys, E4M3, whose codes every wave converts for
+// itself: 1723 us, 486.  What bounds it is one wave's issue, an instruction in 4 cycles, an exponential in 16: of the 4400
+// cycles of a tile 60% are issue, 23% waits for results, 17% waits for LDS and the other waves; the matrix pipes are busy for
+// 49%.  Moving the second product of 32 keys behind the first product of the next 64, so that weights lie beside both, gave 1%
+// and cost E4M3 16%: not kept.
 // An item takes about 12 us besides its tiles of 2 us each (latencies of lengths, pages and keys, 7; code that runs once).
 #include <array>
 #include <cmath>
@@ -76,7 +77,7 @@ constexpr int chunk_lds() {
 template <bool BF16, bool FP8, int D, bool RUNS>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 2 : 1) void chunk_kernel(PagedArgs a) {
   // E4M3: a key's scale enters its weight, which then needs bf16's range, and two parts of it, so that a value is not rounded
-  // by its scale and again as a result.  (1000 rows of 64 heads on to 30001 keys: 1730 us, 1325 with one part.)
+  // by its scale and again as a result.  (1000 rows of 64 heads on to 30001 keys: 1723 us, 1325 with one part.)
   constexpr bool PV_BF16 = BF16 || FP8;
   constexpr float LIFT = !PV_BF16 ? 7.f : 0.f;
   constexpr int RB = FP8 ? D : 2 * D;     // bytes of a cache row

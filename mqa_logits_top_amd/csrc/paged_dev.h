@@ -6,8 +6,9 @@
 // fill the machine, the tiles of a row tile's keys are divided over several workgroups, whose results a second kernel
 // joins.  Lengths are known on the device only, so every workgroup works the division out for itself, from all of them,
 // and finds its own item by a prefix sum over the requests: the items come out equal whatever the lengths are, and a
-// captured launch takes new ones.  64 requests cost a workgroup about 1 us.  Undivided launches find their request by a
-// search in cu_q instead.
+// captured launch takes new ones.  64 requests cost a workgroup about 1 us, and more of them as much for each 64 and, in
+// chunks, each number of parts that is tried (plan_paged has both sides).  Undivided launches find their request by a search
+// in cu_q instead.
 #pragma once
 #include "common.h"
 #include "paged.h"

@@ -2,9 +2,10 @@
 // workgroup, whose four waves divide the keys, 32 at a time, without a barrier until their parts are done.
 //
 // The same pass as paged_chunk.hip's, on 16-row tiles: few rows read every key for little work, so that memory bounds it and
-// waves that never wait for each other keep the most requests under way.  64 rows of 32 heads on 8 of 4100 keys each, bf16:
-// 190 us, 5.6 TB/s (a large copy: 4.7 read and written); 32 of 1700 to 16384, E4M3, pages of 16: 130 us, 4.8 TB/s, and the
-// join, 6.  One row on 4000 keys: 7 us of latencies (lengths, pages, keys, the waves' join), and 4 for the join.
+// waves that never wait for each other keep the most requests under way.  Medians of traced launches: 64 rows of 32 heads on
+// 8 of 4100 keys each, bf16: 189 us, 5.7 TB/s (a large copy: 4.8 read and written); 32 of 1700 to 16384, E4M3, pages of 16:
+// 130 us, 4.8 TB/s, and the join, 6.  One row on 4000 keys: 7.2 us of latencies (lengths, pages, keys, the waves' join), and
+// 4.6 for the join.
 #include <array>
 #include <cmath>
 #include <type_traits>
