@@ -484,6 +484,7 @@ idx_status idx_sparse_attn(const idx_attn *a, void *ws, size_t ws_bytes, void *s
  * page: a power of two; n_pages * page below 2^31; B up to 2^16; T * Hq below 2^26; B * k.H, and the row tiles of a call
  * (T * Hq / 256 + B * k.H, about), below 2^23; with E4M3 caches, or more query heads to a cache head than a row tile takes,
  * those row tiles and 8 k.H together below 2^24.
+ * out may be q itself, with its strides; otherwise out, lse and ws share no byte with the inputs or with each other.
  * ws: idx_paged_attn_workspace() bytes, 256-byte aligned (NULL where that is 0); calls that overlap in time need one
  * each. */
 typedef struct idx_paged {

@@ -131,6 +131,12 @@ int64_t lanes_of(const idx_rows &x) {
 // The scale for powers of two.
 float scale2_of(float scale) { return (float)((double)scale * 1.4426950408889634); }
 
+// Whether two row arrays that start together lie alike; true where they do not.
+bool alike(const idx_rows &a, const idx_rows &b) {
+  return a.data != b.data || (bits(a.dtype) == bits(b.dtype) && (a.T <= 1 || a.ld_t == b.ld_t) &&
+                              (a.H <= 1 || a.ld_h == b.ld_h));
+}
+
 // Queries, outputs and caches of an attention.
 template <class Attn>
 idx_status check_attn_arrays(const Attn *a) {
@@ -179,6 +185,7 @@ idx_status check_paged(const idx_paged *a) {
   if (st) return st;
   if (a->B < 0 || a->n_pages < 0 || a->ld_pages < 0 || a->ld_pages > MAX_LD || (a->B > 1 && a->ld_pages < a->n_pages))
     return IDX_E_SHAPE;
+  if (!alike(a->out, a->q)) return IDX_E_SHAPE;
   if (a->B > MAX_REQUESTS) return IDX_E_UNSUPPORTED;
   if (a->page < 1 || (a->page & (a->page - 1))) return IDX_E_UNSUPPORTED;
   if ((int64_t)a->n_pages * a->page > INT32_MAX) return IDX_E_UNSUPPORTED;
@@ -190,11 +197,6 @@ idx_status check_paged(const idx_paged *a) {
   return plan.max_items < (int64_t)1 << 23 && plan.grid < (int64_t)1 << 24 ? IDX_OK : IDX_E_UNSUPPORTED;
 }
 
-// Whether two row arrays that start together lie alike; true where they do not.
-bool alike(const idx_rows &a, const idx_rows &b) {
-  return a.data != b.data || (bits(a.dtype) == bits(b.dtype) && (a.T <= 1 || a.ld_t == b.ld_t) &&
-                              (a.H <= 1 || a.ld_h == b.ld_h));
-}
 bool same_sizes(const idx_rows &a, const idx_rows &b) { return a.T == b.T && a.H == b.H && a.D == b.D; }
 
 idx_status check_norm(const idx_norm *n) {

@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import mqa_logits_top_amd as idx
-from test_dense_cpu import BF16, FP8, UNSUPPORTED, OK, F, _cache, _paged, _rows
+from test_dense_cpu import BF16, FP8, UNSUPPORTED, OK, SHAPE, F, _cache, _paged, _rows
 
 
 @pytest.mark.parametrize("fmt", [FP8, BF16])
@@ -19,3 +19,13 @@ def test_launches_rounded_up_to_eight_items_stay_below_2_32_lanes(heads, fmt):
     assert lib.idx_paged_attn_workspace(a, ctypes.byref(n)) == (OK if fits else UNSUPPORTED)
     if not fits:
         assert lib.idx_paged_attn(a, F, 1 << 40, None) == UNSUPPORTED
+
+
+def test_results_in_the_queries_place_lie_as_they_do():
+    lib, n = idx.load_library(), ctypes.c_size_t()
+    size = lambda q, out: lib.idx_paged_attn_workspace(_paged(q=q, out=out), ctypes.byref(n))
+    assert size(_rows(), _rows()) == OK and size(_rows(ld_t=2048), _rows(ld_t=2048)) == OK
+    assert size(_rows(ld_t=2048), _rows()) == SHAPE and size(_rows(), _rows(ld_t=2048)) == SHAPE
+    assert lib.idx_paged_attn(_paged(q=_rows(), out=_rows(ld_t=2048)), F, 1 << 40, None) == SHAPE
+    one = dict(T=1)
+    assert size(_rows(ld_t=2048, **one), _rows(**one)) == OK
